@@ -77,9 +77,15 @@ enum moe_status_bits {
   MOE_STATUS_BAD_DOMAIN = 2, /* an RRE domain id was outside 0..G-1 (routed as 0)      */
   MOE_STATUS_BAD_COUNTS = 4, /* expert parallel: a row fell outside its expert's block
                                 (counts that do not match the assignment); skipped     */
-  MOE_STATUS_BAD_INDEX = 8   /* bounds-checked build only (moe_bounds_checked() == 1):
-                                moe_dispatch / moe_combine met an expert index outside
-                                0..E-1 or a slot outside 0..C-1; that choice skipped  */
+  MOE_STATUS_BAD_INDEX = 8,  /* bounds-checked build only (moe_bounds_checked() == 1):
+                                moe_dispatch / moe_combine and their backward passes met
+                                an expert index outside 0..E-1 or a slot outside 0..C-1;
+                                that choice skipped.  moe_route_backward: an index
+                                outside -1..E-1 (in every build), skipped             */
+  MOE_STATUS_BAD_LOGIT = 16, /* moe_route: a logit or bias was NaN or +inf; that expert
+                                was masked                                            */
+  MOE_STATUS_NONFINITE = 32  /* moe_adamw_step: the norm, or the device's step or
+                                learning rate, was not usable; nothing was written    */
 };
 
 /* One MoE layer.  56 bytes, no padding. */
@@ -97,6 +103,35 @@ typedef struct moe_config {
   int32_t reserved;   /* must be 0                                                      */
   uint64_t seed;      /* RRE: seed of the splitmix64 routing hash; ignored for TOPK    */
 } moe_config;
+
+/* How moe_route turns logits into scores and scores into choices.  48 bytes,
+ * no padding. */
+enum moe_score { MOE_SCORE_SOFTMAX = 0, MOE_SCORE_SIGMOID = 1 };
+typedef struct moe_route_config {
+  int64_t T;          /* tokens (>= 0; T * k <= 2^31 - 1)                              */
+  int32_t E;          /* experts, 1..256                                               */
+  int32_t k;          /* choices per token, 1..16, k <= top_groups * E / num_groups     */
+  int32_t score;      /* enum moe_score                                                */
+  int32_t num_groups; /* groups of consecutive experts, 1..32, dividing E              */
+  int32_t top_groups; /* groups a token may choose from, 1..num_groups                 */
+  int32_t group_top;  /* a group's value sums its group_top (1 or 2) best experts;
+                         at most E / num_groups                                        */
+  int32_t renorm;     /* 1: the weights of a token's choices sum to scale              */
+  int32_t dtype;      /* enum moe_dtype of the logits and their gradient               */
+  double scale;       /* factor of every weight, finite                                */
+} moe_route_config;
+
+/* The AdamW step's numbers.  64 bytes, no padding. */
+typedef struct moe_adamw_config {
+  double lr;
+  double beta1, beta2;   /* in [0, 1)                                                  */
+  double eps;            /* a normal positive fp32 number                              */
+  double weight_decay;   /* >= 0                                                       */
+  double max_norm;       /* > 0; read only when a norm is given                        */
+  int64_t step;          /* number of this step, from 1                                */
+  int32_t grad_dtype;    /* enum moe_dtype of the gradients                            */
+  int32_t state_bits;    /* 32 (fp32 moments) or 8                                     */
+} moe_adamw_config;
 
 /* Workspace layout used by moe_layer_forward: byte offsets from the
  * workspace base (each 256-byte aligned) and the total size.  After a call
@@ -127,6 +162,8 @@ int32_t moe_abi_version(void);
 /* sizeof(moe_config) and sizeof(moe_workspace_map) as compiled, for binders. */
 size_t moe_config_size(void);
 size_t moe_workspace_map_size(void);
+size_t moe_route_config_size(void);
+size_t moe_adamw_config_size(void);
 /* Static text for an enum moe_error value. */
 const char* moe_error_string(int32_t code);
 /* Detail of the last error returned on the calling host thread ("" if none). */
@@ -207,6 +244,50 @@ int32_t moe_topk_assign(const moe_config* cfg, const float* logits, const int32_
                         int32_t* n_dropped, void* workspace, size_t workspace_bytes,
                         int32_t* status, moe_stream_t stream);
 
+/* Choices and weights from router logits [T, E] (cfg->dtype), bias [E] fp32
+ * (nullable):
+ *   s[t, e] = softmax over e of the token's logits, or their sigmoid
+ *   c[t, e] = s[t, e] + bias[e]              (bias: enters the choice only)
+ *   top_groups < num_groups: a group's value is the sum of its group_top
+ *     largest c (of those that can be chosen); the top_groups best groups stay
+ *   expert_idx[t, :] = the k largest c of the groups that stay, descending
+ *   gate[t, j] = scale * s[t, e_j], renorm: divided by sum_i s[t, e_i]
+ * Ties go to the lower group and the lower expert.  The order is that of the
+ * exact values: fp32 decides where it can, fp64 where two candidates are too
+ * close for it; without a bias the logits themselves are compared.
+ * Masks: a logit of -inf, or at or below bf16's lowest value (-3.3895e38; so
+ * fp32's lowest too), masks the expert for that token (score 0), a bias of
+ * -inf masks it for every token; NaN and +inf are treated the same and set
+ * MOE_STATUS_BAD_LOGIT.  A masked expert is never chosen: a token with fewer
+ * than k experts left gets expert_idx -1 and gate 0 for the rest (moe_assign
+ * drops such a choice).  Outputs [T, k]: expert_idx int32, gate fp32. */
+int32_t moe_route(const moe_route_config* cfg, const void* logits, const float* bias,
+                  int32_t* expert_idx, float* gate, int32_t* status, moe_stream_t stream);
+
+/* Gradient of moe_route's gates with respect to the logits, the choices held
+ * fixed: from the same logits, expert_idx [T, k] and dgate [T, k] fp32 to
+ * dlogits [T, E] (cfg->dtype, every element written; accumulated in fp32,
+ * rounded once).  A choice of -1 and a masked logit have no gradient; an
+ * expert listed twice for a token gets the sum.  num_groups, top_groups and
+ * group_top do not enter but must be valid. */
+int32_t moe_route_backward(const moe_route_config* cfg, const void* logits,
+                           const int32_t* expert_idx, const float* dgate, void* dlogits,
+                           int32_t* status, moe_stream_t stream);
+
+/* ---- more than two choices --------------------------------------------
+ * moe_assign, moe_dispatch, moe_combine, their backward passes and
+ * moe_ep_ffn_config take configs with k up to 16 (moe_route's choices); every
+ * other call, and moe_config_check, keeps k = 1 or 2.  The expert FFN does not
+ * use k: give it the config that moe_ep_ffn_config(cfg, 1, ...) returns. */
+
+/* Slots for choices made elsewhere: the second half of moe_topk_assign, from
+ * expert_idx [T, k] to slot, kept, tok_of_row, arrivals, kept_cnt and
+ * n_dropped as described there.  A choice outside 0..E-1 (moe_route's -1) gets
+ * slot 2^31 - 1, is not kept, and counts for no expert. */
+int32_t moe_assign(const moe_config* cfg, const int32_t* expert_idx, int32_t* slot, uint8_t* kept,
+                   int32_t* tok_of_row, int32_t* arrivals, int32_t* kept_cnt, int32_t* n_dropped,
+                   int32_t* status, moe_stream_t stream);
+
 /* Dispatch (the permutation the Switch router's dispatch tensor encodes,
  * sec. 2.4): xe[e, s, :] = x[t, :] for every kept choice (t, j) with
  * e = expert_idx[t, j], s = slot[t, j].  Rows of xe that no token fills are
@@ -264,6 +345,26 @@ int32_t moe_expert_ffn_ex(const moe_config* cfg, const void* xe, const void* W1,
 int32_t moe_combine(const moe_config* cfg, const void* ye, const int32_t* expert_idx,
                     const float* gate, const int32_t* slot, const uint8_t* kept, void* y,
                     int32_t* status, moe_stream_t stream);
+
+/* Gradient of moe_dispatch: dx[t, :] = sum over kept j of
+ * dxe[expert_idx[t, j], slot[t, j], :], accumulated in fp32 in choice order and
+ * rounded once; 0 for a token with no kept choice.  dxe [E, C, d], dx [T, d] in
+ * cfg->dtype. */
+int32_t moe_dispatch_backward(const moe_config* cfg, const void* dxe, const int32_t* expert_idx,
+                              const int32_t* slot, const uint8_t* kept, void* dx, int32_t* status,
+                              moe_stream_t stream);
+
+/* Gradient of moe_combine: for every kept choice, with e = expert_idx[t, j],
+ * s = slot[t, j],
+ *   dye[e, s, :] = gate[t, j] * dy[t, :]        rounded once
+ *   dgate[t, j]  = sum over c of dy[t, c] * ye[e, s, c]     fp32
+ * dgate of a choice that was not kept is 0; rows of dye that no token fills are
+ * left untouched.  dy [T, d], ye and dye [E, C, d] in cfg->dtype, dgate [T, k]
+ * fp32.  dye may be ye itself.  The same inputs give the same bits. */
+int32_t moe_combine_backward(const moe_config* cfg, const void* dy, const void* ye,
+                             const int32_t* expert_idx, const float* gate, const int32_t* slot,
+                             const uint8_t* kept, void* dye, float* dgate, int32_t* status,
+                             moe_stream_t stream);
 
 /* The whole layer: router (TOPK) -> gate/top-k or RRE -> slot assignment ->
  * dispatch -> expert FFN -> combine, all on `stream`.  Wr (+ bias) for TOPK,
@@ -354,6 +455,44 @@ int32_t sparseclip_norm_noalloc(const float* const* dense, const int64_t* dense_
                                 int32_t n_dense, const float* const* sparse,
                                 const int64_t* sparse_len, int32_t n_sparse, int32_t num_experts,
                                 double* out, moe_stream_t stream);
+
+/* AdamW over n <= 4096 tensors in place, clipped by the SparseClip norm as the
+ * gradients are read (no pass of its own).  For every element, with t = step:
+ *   g' = g * min(1, max_norm / norm[0])           (norm null: g' = g)
+ *   m  = beta1 m + (1 - beta1) g'
+ *   v  = beta2 v + (1 - beta2) g'^2
+ *   p  = p (1 - lr weight_decay) - lr m^ / (sqrt(v^) + eps),
+ *   m^ = m / (1 - beta1^t),  v^ = v / (1 - beta2^t)
+ * in fp32.  Host arrays of n entries: len (elements); param (device fp32);
+ * grad (device, cfg->grad_dtype); m and v (device); bf16_copy (nullable, and
+ * nullable per entry: receives p rounded to bf16, the layer's weights).
+ * state_bits 32: m and v are fp32 (m_scale, v_scale ignored).
+ * state_bits 8: m and v hold one e4m3 code per element and m_scale, v_scale one
+ * fp32 per block of 256 consecutive elements (the last block may be short):
+ * the first moment is code * scale, the square root of the second is
+ * code * scale.  The step uses the moments of this step before they are
+ * rounded; scale = the block's largest magnitude / 448; a second moment above
+ * 0 is never stored as 0; a first moment is stored as 0 where its block's
+ * largest is below 1e-30.  A NaN or infinite gradient spoils its block.
+ * norm: device double, e.g. sparseclip_norm's out (nullable).  step_lr: device
+ * double[2] = {step, lr} read in place of cfg's (nullable), so that a captured
+ * graph can be replayed with new values.  If norm, step or lr is not finite (or
+ * step < 1) there, nothing is written and MOE_STATUS_NONFINITE is set.
+ * Tensors are 16-byte aligned (scales 4) and must not overlap (moe_adamw_check
+ * tells); zero-length entries are skipped. */
+int32_t moe_adamw_step(const moe_adamw_config* cfg, int32_t n, const int64_t* len,
+                       float* const* param, const void* const* grad, void* const* m,
+                       void* const* v, float* const* m_scale, float* const* v_scale,
+                       void* const* bf16_copy, const double* norm, const double* step_lr,
+                       int32_t* status, moe_stream_t stream);
+
+/* Whether moe_adamw_step takes these tensors, and that nothing it writes
+ * overlaps anything else it reads or writes (a tensor listed twice).  Host
+ * only; lr, step and the other numbers are not looked at. */
+int32_t moe_adamw_check(const moe_adamw_config* cfg, int32_t n, const int64_t* len,
+                        float* const* param, const void* const* grad, void* const* m,
+                        void* const* v, float* const* m_scale, float* const* v_scale,
+                        void* const* bf16_copy);
 
 /* ---- expert parallelism over the GPUs of one node ---------------------- */
 

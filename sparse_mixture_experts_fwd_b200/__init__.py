@@ -26,6 +26,7 @@ ERRORS = {-1: "MOE_ERR_INVALID_ARGUMENT", -2: "MOE_ERR_UNSUPPORTED", -3: "MOE_ER
 DTYPE_BF16, DTYPE_F32 = 0, 1
 ROUTE_TOPK, ROUTE_RRE = 0, 1
 STATUS_TIMEOUT, STATUS_BAD_DOMAIN, STATUS_BAD_COUNTS, STATUS_BAD_INDEX = 1, 2, 4, 8
+STATUS_BAD_LOGIT, STATUS_NONFINITE = 16, 32
 FFN_WORKSPACE_ZEROED = 1
 
 # every entry point the header declares, with its ctypes signature
@@ -48,7 +49,22 @@ class WorkspaceMap(ctypes.Structure):
                                    "total")]
 
 
+class RouteConfig(ctypes.Structure):
+    """Mirror of ``moe_route_config`` (48 bytes)."""
+    _fields_ = [("T", _i64), ("E", _i32), ("k", _i32), ("score", _i32), ("num_groups", _i32),
+                ("top_groups", _i32), ("group_top", _i32), ("renorm", _i32), ("dtype", _i32),
+                ("scale", _dbl)]
+
+
+class AdamWConfig(ctypes.Structure):
+    """Mirror of ``moe_adamw_config`` (64 bytes)."""
+    _fields_ = [("lr", _dbl), ("beta1", _dbl), ("beta2", _dbl), ("eps", _dbl),
+                ("weight_decay", _dbl), ("max_norm", _dbl), ("step", _i64), ("grad_dtype", _i32),
+                ("state_bits", _i32)]
+
+
 _PCFG = ctypes.POINTER(MoEConfig)
+_PRCFG, _PACFG = ctypes.POINTER(RouteConfig), ctypes.POINTER(AdamWConfig)
 _PVP = ctypes.POINTER(ctypes.c_void_p)
 SIGNATURES = {
     "moe_abi_version": ([], _i32),
@@ -81,6 +97,16 @@ SIGNATURES = {
     "sparseclip_norm": ([_vp, _vp, _i32, _vp, _vp, _i32, _i32, _vp, _vp, _sz, _vp], _i32),
     "sparseclip_norm_noalloc": ([_vp, _vp, _i32, _vp, _vp, _i32, _i32, _vp, _vp], _i32),
     "sparseclip_clip": ([_vp, _vp, _i32, _vp, _vp, _i32, _i32, _dbl, _vp, _vp, _sz, _vp], _i32),
+    "moe_route_config_size": ([], _sz),
+    "moe_adamw_config_size": ([], _sz),
+    "moe_route": ([_PRCFG, _vp, _vp, _vp, _vp, _vp, _vp], _i32),
+    "moe_route_backward": ([_PRCFG, _vp, _vp, _vp, _vp, _vp, _vp], _i32),
+    "moe_assign": ([_PCFG, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp], _i32),
+    "moe_dispatch_backward": ([_PCFG, _vp, _vp, _vp, _vp, _vp, _vp, _vp], _i32),
+    "moe_combine_backward": ([_PCFG, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp], _i32),
+    "moe_adamw_check": ([_PACFG, _i32, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp], _i32),
+    "moe_adamw_step": ([_PACFG, _i32, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp],
+                       _i32),
     "moe_ep_ffn_config": ([_PCFG, _i32, _PCFG], _i32),
     "moe_ep_dispatch": ([_PCFG, _i32, _i32, _vp, _vp, _vp, _vp, _vp, _PVP, _vp, _vp, _vp], _i32),
     "moe_ep_combine": ([_PCFG, _i32, _i32, _PVP, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp], _i32),
@@ -99,6 +125,8 @@ def _load_library():
         fn.restype = res
     assert lib.moe_config_size() == ctypes.sizeof(MoEConfig), "moe_config layout mismatch"
     assert lib.moe_workspace_map_size() == ctypes.sizeof(WorkspaceMap), "workspace map mismatch"
+    assert lib.moe_route_config_size() == ctypes.sizeof(RouteConfig), "moe_route_config mismatch"
+    assert lib.moe_adamw_config_size() == ctypes.sizeof(AdamWConfig), "moe_adamw_config mismatch"
     return lib
 
 
@@ -241,6 +269,138 @@ def dispatch(cfg, x, expert_idx, slot, kept, xe=None, status=None, stream=None):
                             _ptr(slot, "slot"), _ptr(kept, "kept"), _ptr(xe, "xe"),
                             _ptr(status, "status"), _stream(stream)), "moe_dispatch")
     return xe
+
+
+def _arg(t, name, dtype, shape):
+    """Device pointer of an argument whose dtype, shape and device are settled."""
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.shape != shape:
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    p = _ptr(t, name)
+    if t.device.index != torch.cuda.current_device():
+        raise ValueError(f"{name} is on {t.device}, the current device is "
+                         f"cuda:{torch.cuda.current_device()}")
+    return p
+
+
+def _empty(shape, dtype, device, stream):
+    """A new output, owned by the stream the call runs on."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
+def _arg_rows(t, name, dtype, rows):
+    """An [E, C, d] buffer, or the same rows as [E * C, d]."""
+    flat = (rows[0] * rows[1], rows[2])
+    return _arg(t, name, dtype, flat if t.dim() == 2 else rows)
+
+
+def _status(status):
+    return None if status is None else _arg(status, "status", torch.int32, (1,))
+
+
+SCORES = {"softmax": 0, "sigmoid": 1}
+
+
+def make_route_config(T, E, k, *, score="softmax", num_groups=1, top_groups=None, group_top=1,
+                      renorm=False, scale=1.0, dtype=torch.float32) -> RouteConfig:
+    """How ``route`` scores and chooses (``moe_route_config``).  ``top_groups``: groups a token
+    may choose from (all of them by default); ``dtype``: the logits'."""
+    return RouteConfig(T=T, E=E, k=k, score=SCORES[score], num_groups=num_groups,
+                       top_groups=num_groups if top_groups is None else top_groups,
+                       group_top=group_top, renorm=int(renorm), dtype=_dtype_code(dtype),
+                       scale=scale)
+
+
+def route(rcfg, logits, bias=None, expert_idx=None, gate=None, status=None, stream=None):
+    """Choices and weights from router logits [T, E]: (expert_idx [T, k] int32, gate [T, k] fp32).
+
+    ``bias`` [E] fp32 enters the choice only.  A token with fewer than k experts
+    left (the others masked by -inf) gets -1 and weight 0 for the rest."""
+    T, E, k = rcfg.T, rcfg.E, rcfg.k
+    lp = _arg(logits, "logits", _act_dtype(rcfg), (T, E))
+    bp = None if bias is None else _arg(bias, "bias", torch.float32, (E,))
+    if expert_idx is None:
+        expert_idx = _empty((T, k), torch.int32, logits.device, stream)
+    if gate is None:
+        gate = _empty((T, k), torch.float32, logits.device, stream)
+    _check(lib.moe_route(ctypes.byref(rcfg), lp, bp,
+                         _arg(expert_idx, "expert_idx", torch.int32, (T, k)),
+                         _arg(gate, "gate", torch.float32, (T, k)), _status(status),
+                         _stream(stream)), "moe_route")
+    return expert_idx, gate
+
+
+def route_backward(rcfg, logits, expert_idx, dgate, dlogits=None, status=None, stream=None):
+    """Gradient of ``route``'s weights with respect to the logits, the choices held fixed."""
+    T, E, k = rcfg.T, rcfg.E, rcfg.k
+    lp = _arg(logits, "logits", _act_dtype(rcfg), (T, E))
+    if dlogits is None:
+        dlogits = _empty((T, E), logits.dtype, logits.device, stream)
+    _check(lib.moe_route_backward(ctypes.byref(rcfg), lp,
+                                  _arg(expert_idx, "expert_idx", torch.int32, (T, k)),
+                                  _arg(dgate, "dgate", torch.float32, (T, k)),
+                                  _arg(dlogits, "dlogits", logits.dtype, (T, E)),
+                                  _status(status), _stream(stream)), "moe_route_backward")
+    return dlogits
+
+
+def assign(cfg, expert_idx, out=None, status=None, stream=None):
+    """Slots for given choices [T, k], k up to 16.  Returns a dict: slot, kept, tok_of_row
+    [E * C], arrivals, kept_cnt, n_dropped (``out`` may supply any of them)."""
+    T, k, E, C = cfg.T, cfg.k, cfg.E, cfg.capacity
+    ep = _arg(expert_idx, "expert_idx", torch.int32, (T, k))
+    o = {} if out is None else out
+    ptrs = []
+    for name, dtype, shape in (("slot", torch.int32, (T, k)), ("kept", torch.uint8, (T, k)),
+                               ("tok_of_row", torch.int32, (E * C,)),
+                               ("arrivals", torch.int32, (E,)), ("kept_cnt", torch.int32, (E,)),
+                               ("n_dropped", torch.int32, (1,))):
+        if name not in o:
+            o[name] = _empty(shape, dtype, expert_idx.device, stream)
+        ptrs.append(_arg(o[name], name, dtype, shape))
+    _check(lib.moe_assign(ctypes.byref(cfg), ep, *ptrs, _status(status), _stream(stream)),
+           "moe_assign")
+    return o
+
+
+def dispatch_backward(cfg, dxe, expert_idx, slot, kept, dx=None, status=None, stream=None):
+    """Gradient of ``dispatch``: dx [T, d] sums the kept choices' rows of dxe [E, C, d]."""
+    T, k, act = cfg.T, cfg.k, _act_dtype(cfg)
+    if dx is None:
+        dx = _empty((T, cfg.d_model), act, dxe.device, stream)
+    _check(lib.moe_dispatch_backward(
+        ctypes.byref(cfg), _arg_rows(dxe, "dxe", act, (cfg.E, cfg.capacity, cfg.d_model)),
+        _arg(expert_idx, "expert_idx", torch.int32, (T, k)),
+        _arg(slot, "slot", torch.int32, (T, k)), _arg(kept, "kept", torch.uint8, (T, k)),
+        _arg(dx, "dx", act, (T, cfg.d_model)), _status(status), _stream(stream)),
+        "moe_dispatch_backward")
+    return dx
+
+
+def combine_backward(cfg, dy, ye, expert_idx, gate, slot, kept, dye=None, dgate=None, status=None,
+                     stream=None):
+    """Gradients of ``combine``: (dye [E, C, d], dgate [T, k]).  Rows of ``dye`` that no token
+    fills are left as they are (zeros in a ``dye`` made here); ``dye`` may be ``ye``."""
+    T, k, act = cfg.T, cfg.k, _act_dtype(cfg)
+    rows = (cfg.E, cfg.capacity, cfg.d_model)
+    if dye is None:
+        dye = _empty(rows, act, ye.device, stream)
+        with torch.cuda.stream(stream):
+            dye.zero_()
+    if dgate is None:
+        dgate = _empty((T, k), torch.float32, ye.device, stream)
+    _check(lib.moe_combine_backward(
+        ctypes.byref(cfg), _arg(dy, "dy", act, (T, cfg.d_model)), _arg_rows(ye, "ye", act, rows),
+        _arg(expert_idx, "expert_idx", torch.int32, (T, k)),
+        _arg(gate, "gate", torch.float32, (T, k)), _arg(slot, "slot", torch.int32, (T, k)),
+        _arg(kept, "kept", torch.uint8, (T, k)), _arg_rows(dye, "dye", act, rows),
+        _arg(dgate, "dgate", torch.float32, (T, k)), _status(status), _stream(stream)),
+        "moe_combine_backward")
+    return dye, dgate
 
 
 def ffn_workspace_size(cfg: MoEConfig) -> int:
@@ -460,3 +620,107 @@ def sparseclip_clip(dense, sparse, num_experts, max_norm, out=None, workspace=No
                                _ptr(workspace, "workspace"), workspace.numel(), _stream(stream)),
            "sparseclip_clip")
     return out
+
+
+Q_BLOCK = 256  # elements of a tensor that share one scale of the 8-bit moments
+
+
+def adamw_state(params, bits=32):
+    """Zero moments for a list of fp32 parameters, as keyword arguments of ``adamw_tensors``:
+    fp32 (bits=32), or e4m3 codes with one fp32 scale per 256 elements (bits=8)."""
+    if bits not in (32, 8):
+        raise ValueError("bits must be 32 or 8")
+
+    def zeros(dtype, blocks=False):
+        return [torch.zeros(-(-p.numel() // Q_BLOCK) if blocks else p.numel(), dtype=dtype,
+                            device=p.device) for p in params]
+
+    if bits == 32:
+        return dict(exp_avg=zeros(torch.float32), exp_avg_sq=zeros(torch.float32))
+    return dict(exp_avg=zeros(torch.float8_e4m3fn), exp_avg_sq=zeros(torch.float8_e4m3fn),
+                exp_avg_scale=zeros(torch.float32, True),
+                exp_avg_sq_scale=zeros(torch.float32, True))
+
+
+class AdamWTensors:
+    """The tensors of an AdamW step, checked and laid out once (``adamw_tensors``).  It holds
+    on to the tensors; a step reads and writes the memory they had when it was made."""
+
+    def __init__(self, n, device, grad_dtype, bits, arrays, keep):
+        self.n, self.device, self.grad_dtype, self.bits = n, device, grad_dtype, bits
+        self.arrays, self.keep = arrays, keep
+
+
+def adamw_tensors(params, grads, exp_avg, exp_avg_sq, *, exp_avg_scale=None,
+                  exp_avg_sq_scale=None, bf16_copies=None) -> AdamWTensors:
+    """Lists of tensors for ``adamw_step``: fp32 ``params``; ``grads`` all fp32 or all bf16;
+    the moments fp32, or float8_e4m3fn with their fp32 scales (one per 256 elements);
+    ``bf16_copies`` (optional, entries may be None) receive the new parameters in bf16.  All
+    contiguous, on one device, with the parameter's number of elements; nothing that the
+    step writes may overlap anything else."""
+    params, grads = list(params), list(grads)
+    n = len(params)
+    dev = params[0].device if n else None
+    gdt = grads[0].dtype if grads else torch.float32
+    exp_avg, exp_avg_sq = list(exp_avg), list(exp_avg_sq)
+    bits = 8 if exp_avg and exp_avg[0].dtype == torch.float8_e4m3fn else 32
+    if bits == 8 and (exp_avg_scale is None or exp_avg_sq_scale is None):
+        raise ValueError("8-bit moments need exp_avg_scale and exp_avg_sq_scale")
+    sdt = torch.float8_e4m3fn if bits == 8 else torch.float32
+    numel = [p.numel() for p in params]
+    blocks = [-(-m // Q_BLOCK) for m in numel]
+
+    def pointers(ts, name, dtype, sizes, optional=False):
+        ts = list(ts)
+        if len(ts) != n:
+            raise ValueError(f"{name} needs {n} entries, got {len(ts)}")
+        out = (ctypes.c_void_p * max(1, n))()
+        for i, t in enumerate(ts):
+            if t is None and optional:
+                continue
+            if t.dtype != dtype:
+                raise TypeError(f"{name}[{i}] must be {dtype}, got {t.dtype}")
+            if t.numel() != sizes[i]:
+                raise ValueError(f"{name}[{i}] must have {sizes[i]} elements, got {t.numel()}")
+            if t.device != dev:
+                raise ValueError(f"{name}[{i}] is on {t.device}, params[0] on {dev}")
+            out[i] = _ptr(t, f"{name}[{i}]")
+        return out, ts
+
+    made = [pointers(params, "params", torch.float32, numel),
+            pointers(grads, "grads", gdt, numel),
+            pointers(exp_avg, "exp_avg", sdt, numel),
+            pointers(exp_avg_sq, "exp_avg_sq", sdt, numel)]
+    made += ([pointers(exp_avg_scale, "exp_avg_scale", torch.float32, blocks),
+              pointers(exp_avg_sq_scale, "exp_avg_sq_scale", torch.float32, blocks)]
+             if bits == 8 else [(None, None), (None, None)])
+    made.append((None, None) if bf16_copies is None else
+                pointers(bf16_copies, "bf16_copies", torch.bfloat16, numel, optional=True))
+    lens = (ctypes.c_int64 * max(1, n))(*numel)
+    arrays = [ctypes.cast(lens, _vp)] + [None if a is None else ctypes.cast(a, _vp)
+                                         for a, _ in made]
+    cfg = AdamWConfig(grad_dtype=_dtype_code(gdt), state_bits=bits)
+    _check(lib.moe_adamw_check(ctypes.byref(cfg), n, *arrays), "moe_adamw_check")
+    return AdamWTensors(n, dev, cfg.grad_dtype, bits, arrays, (lens, made))
+
+
+def adamw_step(tensors, *, step=1, lr=1e-3, betas=(0.9, 0.999), eps=1e-8, weight_decay=1e-2,
+               norm=None, max_norm=0.0, step_lr=None, status=None, stream=None):
+    """One AdamW step over ``tensors`` (``adamw_tensors``), in place.
+
+    ``norm``: float64 device tensor whose first element is the gradients' norm (the output of
+    ``sparseclip_norm``); the gradients are scaled by min(1, max_norm / norm) as they are read.
+    ``step_lr``: float64 device tensor (step, lr) read instead of ``step`` and ``lr``, for a
+    step captured into a CUDA graph."""
+    if tensors.n and tensors.device.index != torch.cuda.current_device():
+        raise ValueError(f"the tensors are on {tensors.device}, the current device is "
+                         f"cuda:{torch.cuda.current_device()}")
+    np_ = None if norm is None else _arg(norm, "norm", torch.float64, norm.shape)
+    sp = None if step_lr is None else _arg(step_lr, "step_lr", torch.float64, (2,))
+    if norm is not None and norm.numel() < 1:
+        raise ValueError("norm is empty")
+    cfg = AdamWConfig(lr=lr, beta1=betas[0], beta2=betas[1], eps=eps, weight_decay=weight_decay,
+                      max_norm=max_norm, step=step, grad_dtype=tensors.grad_dtype,
+                      state_bits=tensors.bits)
+    _check(lib.moe_adamw_step(ctypes.byref(cfg), tensors.n, *tensors.arrays, np_, sp,
+                              _status(status), _stream(stream)), "moe_adamw_step")

@@ -49,12 +49,15 @@ namespace {
 
 constexpr int64_t kI32Max = 2147483647;
 
-int32_t check_cfg(const moe_config* c) {
+// max_k: 2, or kMaxChoices for the calls that only move rows
+int32_t check_cfg(const moe_config* c, int32_t max_k = 2) {
   if (!c) return fail(MOE_ERR_INVALID_ARGUMENT, "config is null");
   if (c->T < 0 || c->T > kI32Max) return fail(MOE_ERR_INVALID_ARGUMENT, "T out of range");
   if (c->E < 1) return fail(MOE_ERR_INVALID_ARGUMENT, "E < 1");
   if (c->E > 256) return fail(MOE_ERR_UNSUPPORTED, "E > 256");
-  if (c->k != 1 && c->k != 2) return fail(MOE_ERR_UNSUPPORTED, "k must be 1 or 2");
+  if (c->k < 1 || c->k > max_k)
+    return fail(MOE_ERR_UNSUPPORTED,
+                max_k == 2 ? "k must be 1 or 2" : "k must be 1.." + std::to_string(max_k));
   if (c->k > c->E) return fail(MOE_ERR_INVALID_ARGUMENT, "k > E");
   if (c->capacity < 0) return fail(MOE_ERR_INVALID_ARGUMENT, "capacity < 0");
   if (c->dtype != MOE_DTYPE_BF16 && c->dtype != MOE_DTYPE_F32)
@@ -83,6 +86,34 @@ int32_t check_cfg(const moe_config* c) {
   if (EC > kI32Max || int64_t(c->E) * c->d_ff * 2 > kI32Max || int64_t(c->E) * c->d_model > kI32Max)
     return fail(MOE_ERR_UNSUPPORTED, "E*C, E*d_ff or E*d_model exceeds 2^31-1 rows");
   // per-expert arrival counts, slots and the choice index are 32-bit
+  if (c->T * c->k > kI32Max) return fail(MOE_ERR_UNSUPPORTED, "T*k exceeds 2^31-1 choices");
+  return MOE_OK;
+}
+
+int32_t check_route(const moe_route_config* c) {
+  if (!c) return fail(MOE_ERR_INVALID_ARGUMENT, "config is null");
+  if (c->T < 0 || c->T > kI32Max) return fail(MOE_ERR_INVALID_ARGUMENT, "T out of range");
+  if (c->E < 1) return fail(MOE_ERR_INVALID_ARGUMENT, "E < 1");
+  if (c->E > 256) return fail(MOE_ERR_UNSUPPORTED, "E > 256");
+  if (c->k < 1 || c->k > kMaxChoices)
+    return fail(MOE_ERR_UNSUPPORTED, "k must be 1.." + std::to_string(kMaxChoices));
+  if (c->score != MOE_SCORE_SOFTMAX && c->score != MOE_SCORE_SIGMOID)
+    return fail(MOE_ERR_INVALID_ARGUMENT, "unknown score");
+  if (c->num_groups < 1 || c->E % c->num_groups != 0)
+    return fail(MOE_ERR_INVALID_ARGUMENT, "num_groups must be >= 1 and divide E");
+  if (c->num_groups > 32) return fail(MOE_ERR_UNSUPPORTED, "num_groups > 32");
+  if (c->top_groups < 1 || c->top_groups > c->num_groups)
+    return fail(MOE_ERR_INVALID_ARGUMENT, "top_groups must be 1..num_groups");
+  const int32_t per = c->E / c->num_groups;
+  if (c->group_top < 1 || c->group_top > 2 || c->group_top > per)
+    return fail(MOE_ERR_INVALID_ARGUMENT, "group_top must be 1 or 2 and at most E / num_groups");
+  if (c->k > c->top_groups * per)
+    return fail(MOE_ERR_INVALID_ARGUMENT, "k > top_groups * E / num_groups");
+  if (c->renorm != 0 && c->renorm != 1) return fail(MOE_ERR_INVALID_ARGUMENT, "renorm must be 0 or 1");
+  if (c->dtype != MOE_DTYPE_BF16 && c->dtype != MOE_DTYPE_F32)
+    return fail(MOE_ERR_INVALID_ARGUMENT, "unknown dtype");
+  if (!std::isfinite(static_cast<float>(c->scale)))
+    return fail(MOE_ERR_INVALID_ARGUMENT, "scale is not a finite fp32 number");
   if (c->T * c->k > kI32Max) return fail(MOE_ERR_UNSUPPORTED, "T*k exceeds 2^31-1 choices");
   return MOE_OK;
 }
@@ -148,6 +179,7 @@ extern "C" {
 int32_t moe_abi_version(void) { return MOE_ABI_VERSION; }
 size_t moe_config_size(void) { return sizeof(moe_config); }
 size_t moe_workspace_map_size(void) { return sizeof(moe_workspace_map); }
+size_t moe_route_config_size(void) { return sizeof(moe_route_config); }
 
 const char* moe_error_string(int32_t code) {
   switch (code) {
@@ -252,13 +284,16 @@ int32_t moe_dispatch(const moe_config* cfg, const void* x, const int32_t* expert
                      moe_stream_t stream) {
   CallRange range_("moe_dispatch");
   set_last_error("");
-  MOE_TRY(check_cfg(cfg));
+  MOE_TRY(check_cfg(cfg, kMaxChoices));
   if (cfg->T == 0 || cfg->capacity == 0) return MOE_OK;
   MOE_TRY(need_ptr(x, "x"));
   MOE_TRY(need_ptr4(expert_idx, "expert_idx"));
   MOE_TRY(need_ptr4(slot, "slot"));
   if (!kept) return fail(MOE_ERR_INVALID_ARGUMENT, "kept is null");
   MOE_TRY(need_ptr(xe, "xe"));
+  if (cfg->k > 2)
+    return launch_scatter_choices(*cfg, x, expert_idx, slot, kept, xe, status,
+                                  reinterpret_cast<cudaStream_t>(stream));
   return launch_dispatch(*cfg, x, expert_idx, slot, kept, xe, status,
                          reinterpret_cast<cudaStream_t>(stream));
 }
@@ -308,7 +343,7 @@ int32_t moe_combine(const moe_config* cfg, const void* ye, const int32_t* expert
                     int32_t* status, moe_stream_t stream) {
   CallRange range_("moe_combine");
   set_last_error("");
-  MOE_TRY(check_cfg(cfg));
+  MOE_TRY(check_cfg(cfg, kMaxChoices));
   if (cfg->T == 0) return MOE_OK;
   if (cfg->capacity > 0) MOE_TRY(need_ptr(ye, "ye"));
   MOE_TRY(need_ptr4(expert_idx, "expert_idx"));
@@ -316,8 +351,98 @@ int32_t moe_combine(const moe_config* cfg, const void* ye, const int32_t* expert
   MOE_TRY(need_ptr4(slot, "slot"));
   if (!kept) return fail(MOE_ERR_INVALID_ARGUMENT, "kept is null");
   MOE_TRY(need_ptr(y, "y"));
+  if (cfg->k > 2)
+    return launch_gather_choices(*cfg, ye, expert_idx, gate, slot, kept, y, status,
+                                 reinterpret_cast<cudaStream_t>(stream));
   return launch_combine(*cfg, ye, expert_idx, gate, slot, kept, y, status,
                         reinterpret_cast<cudaStream_t>(stream));
+}
+
+int32_t moe_dispatch_backward(const moe_config* cfg, const void* dxe, const int32_t* expert_idx,
+                              const int32_t* slot, const uint8_t* kept, void* dx, int32_t* status,
+                              moe_stream_t stream) {
+  CallRange range_("moe_dispatch_backward");
+  set_last_error("");
+  MOE_TRY(check_cfg(cfg, kMaxChoices));
+  if (cfg->T == 0) return MOE_OK;
+  if (cfg->capacity > 0) MOE_TRY(need_ptr(dxe, "dxe"));
+  MOE_TRY(need_ptr4(expert_idx, "expert_idx"));
+  MOE_TRY(need_ptr4(slot, "slot"));
+  if (!kept) return fail(MOE_ERR_INVALID_ARGUMENT, "kept is null");
+  MOE_TRY(need_ptr(dx, "dx"));
+  return launch_gather_choices(*cfg, dxe, expert_idx, nullptr, slot, kept, dx, status,
+                               reinterpret_cast<cudaStream_t>(stream));
+}
+
+int32_t moe_combine_backward(const moe_config* cfg, const void* dy, const void* ye,
+                             const int32_t* expert_idx, const float* gate, const int32_t* slot,
+                             const uint8_t* kept, void* dye, float* dgate, int32_t* status,
+                             moe_stream_t stream) {
+  CallRange range_("moe_combine_backward");
+  set_last_error("");
+  MOE_TRY(check_cfg(cfg, kMaxChoices));
+  if (cfg->T == 0) return MOE_OK;
+  MOE_TRY(need_ptr(dy, "dy"));
+  if (cfg->capacity > 0) {
+    MOE_TRY(need_ptr(ye, "ye"));
+    MOE_TRY(need_ptr(dye, "dye"));
+  }
+  MOE_TRY(need_ptr4(expert_idx, "expert_idx"));
+  MOE_TRY(need_ptr4(gate, "gate"));
+  MOE_TRY(need_ptr4(slot, "slot"));
+  if (!kept) return fail(MOE_ERR_INVALID_ARGUMENT, "kept is null");
+  MOE_TRY(need_ptr4(dgate, "dgate"));
+  return launch_combine_backward(*cfg, dy, ye, expert_idx, gate, slot, kept, dye, dgate, status,
+                                 reinterpret_cast<cudaStream_t>(stream));
+}
+
+int32_t moe_route(const moe_route_config* cfg, const void* logits, const float* bias,
+                  int32_t* expert_idx, float* gate, int32_t* status, moe_stream_t stream) {
+  CallRange range_("moe_route");
+  set_last_error("");
+  MOE_TRY(check_route(cfg));
+  if (cfg->T == 0) return MOE_OK;
+  MOE_TRY(need_ptr(logits, "logits"));
+  if (bias) MOE_TRY(need_ptr4(bias, "bias"));
+  MOE_TRY(need_ptr4(expert_idx, "expert_idx"));
+  MOE_TRY(need_ptr4(gate, "gate"));
+  return launch_route(*cfg, logits, bias, expert_idx, gate, status,
+                      reinterpret_cast<cudaStream_t>(stream));
+}
+
+int32_t moe_route_backward(const moe_route_config* cfg, const void* logits,
+                           const int32_t* expert_idx, const float* dgate, void* dlogits,
+                           int32_t* status, moe_stream_t stream) {
+  CallRange range_("moe_route_backward");
+  set_last_error("");
+  MOE_TRY(check_route(cfg));
+  if (cfg->T == 0) return MOE_OK;
+  MOE_TRY(need_ptr(logits, "logits"));
+  MOE_TRY(need_ptr4(expert_idx, "expert_idx"));
+  MOE_TRY(need_ptr4(dgate, "dgate"));
+  MOE_TRY(need_ptr(dlogits, "dlogits"));
+  if (dlogits == logits) return fail(MOE_ERR_INVALID_ARGUMENT, "dlogits is logits");
+  return launch_route_backward(*cfg, logits, expert_idx, dgate, dlogits, status,
+                               reinterpret_cast<cudaStream_t>(stream));
+}
+
+int32_t moe_assign(const moe_config* cfg, const int32_t* expert_idx, int32_t* slot, uint8_t* kept,
+                   int32_t* tok_of_row, int32_t* arrivals, int32_t* kept_cnt, int32_t* n_dropped,
+                   int32_t* status, moe_stream_t stream) {
+  CallRange range_("moe_assign");
+  set_last_error("");
+  MOE_TRY(check_cfg(cfg, kMaxChoices));
+  if (cfg->T > 0) {
+    MOE_TRY(need_ptr4(expert_idx, "expert_idx"));
+    MOE_TRY(need_ptr4(slot, "slot"));
+    if (!kept) return fail(MOE_ERR_INVALID_ARGUMENT, "kept is null");
+  }
+  if (int64_t(cfg->E) * cfg->capacity > 0) MOE_TRY(need_ptr4(tok_of_row, "tok_of_row"));
+  MOE_TRY(need_ptr4(arrivals, "arrivals"));
+  MOE_TRY(need_ptr4(kept_cnt, "kept_cnt"));
+  MOE_TRY(need_ptr4(n_dropped, "n_dropped"));
+  return launch_assign(*cfg, expert_idx, slot, kept, tok_of_row, arrivals, kept_cnt, n_dropped,
+                       nullptr, status, reinterpret_cast<cudaStream_t>(stream));
 }
 
 size_t moe_aux_workspace_size(const moe_config* cfg) {
@@ -441,8 +566,8 @@ int32_t moe_layer_forward(const moe_config* cfg, const void* x, const void* Wr, 
 
 namespace {
 
-int32_t check_ep(const moe_config* cfg, int32_t rank, int32_t world) {
-  MOE_TRY(check_cfg(cfg));
+int32_t check_ep(const moe_config* cfg, int32_t rank, int32_t world, int32_t max_k = 2) {
+  MOE_TRY(check_cfg(cfg, max_k));
   if (world < 1 || world > kMaxEpRanks)
     return fail(MOE_ERR_INVALID_ARGUMENT, "world must be 1.." + std::to_string(kMaxEpRanks));
   if (rank < 0 || rank >= world) return fail(MOE_ERR_INVALID_ARGUMENT, "rank outside 0..world-1");
@@ -463,7 +588,7 @@ int32_t check_peers(const void* const* peers, int32_t world, const char* name) {
 
 int32_t moe_ep_ffn_config(const moe_config* cfg, int32_t world, moe_config* out) {
   set_last_error("");
-  MOE_TRY(check_ep(cfg, 0, world));
+  MOE_TRY(check_ep(cfg, 0, world, kMaxChoices));
   if (!out) return fail(MOE_ERR_INVALID_ARGUMENT, "out is null");
   moe_config c = *cfg;
   c.E = cfg->E / world;

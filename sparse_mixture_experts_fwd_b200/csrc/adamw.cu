@@ -1,0 +1,512 @@
+// AdamW over many tensors in one call, with the moments in fp32 or in 8 bits,
+// the gradients scaled by the SparseClip coefficient as they are read.
+//
+//   c  = min(1, max_norm / norm)                (norm: a device double, or c = 1)
+//   m  = b1 m + (1 - b1) c g
+//   v  = b2 v + (1 - b2) (c g)^2
+//   p -= lr wd p + lr / (1 - b1^t) * m / (sqrt(v) / sqrt(1 - b2^t) + eps)
+//
+// 8-bit moments: every 256 consecutive elements of a tensor share one fp32
+// scale per moment.  m is kept as e4m3 codes of m / scale with scale =
+// max|m| / 448; v as e4m3 codes of sqrt(v) / scale, scale = max sqrt(v) / 448,
+// so that its 18 binades cover 36 of v, and a v > 0 never falls below the
+// smallest code: a step divided by a second moment that was rounded to zero
+// would be unbounded, one divided by a moment rounded up is only shorter.
+#include <algorithm>
+#include <cfloat>
+#include <cmath>
+#include <vector>
+
+#include "moe_internal.cuh"
+
+namespace moe {
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kQBlock = 256;         // elements per scale: 8 per lane of one warp
+constexpr int kChunk = 2048;         // elements per block and round: 8 per thread
+constexpr int kMaxTensors = 4096;
+constexpr int kSmallBatch = 32;      // tensors in the small launch parameter block
+constexpr int kLargeBatch = 384;     // and in the large one (27 KB of the 32 KB limit)
+// An |m| maximum below this stores the block's m as zeros: its scale's
+// reciprocal would leave fp32's range.
+constexpr float kTiny = 1e-30f;
+
+struct AdamTensor {
+  float* p;
+  const void* g;
+  void* m;
+  void* v;
+  float* ms;
+  float* vs;
+  __nv_bfloat16* copy;
+  int64_t len;
+};
+
+struct AdamHyper {
+  float b1, nb1, b2, nb2, eps;      // nb = 1 - b, rounded from the double
+  double lr, wd, step;
+  double beta1, beta2;
+  double max_norm;
+  const double* norm;               // nullable
+  const double* step_lr;            // nullable: {step, lr} on the device
+  int32_t* status;
+};
+
+template <int N>
+struct AdamBatch {
+  AdamTensor t[N];
+  int32_t first[N + 1];             // first chunk of each tensor; first[n] = chunks in all
+  int32_t n;
+};
+
+struct StepScalars {
+  float clip, decay, rate, root;    // root = 1 / sqrt(1 - b2^t)
+  int skip;
+};
+
+MOE_DEV float sqrt_fast(float x) {
+  // off by at most 2^-23 relative, which changes the length of a step by as much
+  float r;
+  asm("sqrt.approx.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+
+// p, m, v (fp32) -> their next values; returns sqrt(v)
+MOE_DEV float adam_one(float& p, float g, float& m, float& v, const AdamHyper& h,
+                       const StepScalars& s) {
+  g *= s.clip;
+  m = fmaf(h.b1, m, h.nb1 * g);
+  v = fmaf(h.b2, v, h.nb2 * g * g);
+  const float r = sqrt_fast(v);
+  p = fmaf(-s.rate, __fdividef(m, fmaf(r, s.root, h.eps)), p * s.decay);
+  return r;
+}
+
+MOE_DEV void load4(const float* p, float (&f)[4]) {
+  const float4 v = *reinterpret_cast<const float4*>(p);
+  f[0] = v.x; f[1] = v.y; f[2] = v.z; f[3] = v.w;
+}
+MOE_DEV void load4(const __nv_bfloat16* p, float (&f)[4]) {
+  const uint2 v = *reinterpret_cast<const uint2*>(p);
+  f[0] = __uint_as_float(v.x << 16); f[1] = __uint_as_float(v.x & 0xffff0000u);
+  f[2] = __uint_as_float(v.y << 16); f[3] = __uint_as_float(v.y & 0xffff0000u);
+}
+MOE_DEV void store4(float* p, const float (&f)[4]) {
+  *reinterpret_cast<float4*>(p) = make_float4(f[0], f[1], f[2], f[3]);
+}
+MOE_DEV void store4(__nv_bfloat16* p, const float (&f)[4]) {
+  __nv_bfloat162 a = __floats2bfloat162_rn(f[0], f[1]), b = __floats2bfloat162_rn(f[2], f[3]);
+  *reinterpret_cast<uint2*>(p) =
+      make_uint2(*reinterpret_cast<uint32_t*>(&a), *reinterpret_cast<uint32_t*>(&b));
+}
+MOE_DEV float load1(const float* p) { return *p; }
+MOE_DEV float load1(const __nv_bfloat16* p) { return __bfloat162float(*p); }
+
+// four e4m3 codes <-> four floats
+MOE_DEV void of_e4m3x4(uint32_t q, float (&f)[4]) {
+  uint32_t lo, hi;
+  asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\t"
+      "cvt.rn.f16x2.e4m3x2 %0, a;\n\tcvt.rn.f16x2.e4m3x2 %1, b;\n\t}"
+      : "=r"(lo), "=r"(hi)
+      : "r"(q));
+  asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\tcvt.f32.f16 %0, a;\n\tcvt.f32.f16 %1, b;\n\t}"
+      : "=f"(f[0]), "=f"(f[1])
+      : "r"(lo));
+  asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\tcvt.f32.f16 %0, a;\n\tcvt.f32.f16 %1, b;\n\t}"
+      : "=f"(f[2]), "=f"(f[3])
+      : "r"(hi));
+}
+MOE_DEV uint32_t to_e4m3x4(const float (&f)[4]) {
+  uint32_t q;
+  asm("{\n\t.reg .b16 a, b;\n\tcvt.rn.satfinite.e4m3x2.f32 a, %2, %1;\n\t"
+      "cvt.rn.satfinite.e4m3x2.f32 b, %4, %3;\n\tmov.b32 %0, {a, b};\n\t}"
+      : "=r"(q)
+      : "f"(f[0]), "f"(f[1]), "f"(f[2]), "f"(f[3]));
+  return q;
+}
+
+// The step's scalars, the same in every block.  Formed in fp64: 1 - b^t loses
+// its leading digits for b near 1 and small t.
+MOE_DEV StepScalars step_scalars(const AdamHyper& h) {
+  StepScalars s;
+  double t = h.step, lr = h.lr;
+  bool ok = true;
+  if (h.step_lr) {
+    t = h.step_lr[0];
+    lr = h.step_lr[1];
+    ok = t >= 1.0 && isfinite(t) && isfinite(lr);
+  }
+  double clip = 1.0;
+  if (h.norm) {
+    const double n = *h.norm;
+    ok = ok && isfinite(n);
+    if (n > h.max_norm) clip = h.max_norm / n;
+  }
+  s.clip = static_cast<float>(clip);
+  s.decay = static_cast<float>(1.0 - lr * h.wd);
+  s.rate = static_cast<float>(lr / (1.0 - pow(h.beta1, t)));
+  s.root = static_cast<float>(1.0 / sqrt(1.0 - pow(h.beta2, t)));
+  s.skip = !ok;
+  return s;
+}
+
+// tensor of chunk c (last i with first[i] <= c)
+template <int N>
+MOE_DEV int tensor_of(const AdamBatch<N>& b, int c) {
+  int lo = 0, hi = b.n - 1;
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if (b.first[mid] <= c) lo = mid;
+    else hi = mid - 1;
+  }
+  return lo;
+}
+
+// A round handles kChunk elements: thread i takes the 4 at 4 i and the 4 at
+// 1024 + 4 i, so that every load of a warp is one contiguous run.
+template <typename G, int N>
+__global__ void __launch_bounds__(kThreads)
+adamw_kernel(const __grid_constant__ AdamBatch<N> b, const AdamHyper h) {
+  __shared__ StepScalars s_step;
+  dev::pdl_trigger();
+  dev::pdl_wait();
+  if (threadIdx.x == 0) s_step = step_scalars(h);
+  __syncthreads();
+  const StepScalars s = s_step;
+  if (s.skip) {
+    if (blockIdx.x == 0 && threadIdx.x == 0 && h.status) atomicOr(h.status, MOE_STATUS_NONFINITE);
+    return;
+  }
+  for (int c = blockIdx.x; c < b.first[b.n]; c += gridDim.x) {
+    const int n = tensor_of(b, c);
+    const AdamTensor& t = b.t[n];
+    const int64_t base = static_cast<int64_t>(c - b.first[n]) * kChunk;
+    float* p = t.p;
+    const G* g = static_cast<const G*>(t.g);
+    float* m = static_cast<float*>(t.m);
+    float* v = static_cast<float*>(t.v);
+    float fp[2][4], fg[2][4], fm[2][4], fv[2][4];
+    if (base + kChunk <= t.len) {
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        const int64_t i = base + u * (kThreads * 4) + threadIdx.x * 4;
+        load4(p + i, fp[u]);
+        load4(g + i, fg[u]);
+        load4(m + i, fm[u]);
+        load4(v + i, fv[u]);
+      }
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        const int64_t i = base + u * (kThreads * 4) + threadIdx.x * 4;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) adam_one(fp[u][k], fg[u][k], fm[u][k], fv[u][k], h, s);
+        store4(p + i, fp[u]);
+        store4(m + i, fm[u]);
+        store4(v + i, fv[u]);
+        if (t.copy) store4(t.copy + i, fp[u]);
+      }
+    } else {
+      for (int64_t i = base + threadIdx.x; i < t.len; i += kThreads) {
+        float x = p[i], y = m[i], z = v[i];
+        adam_one(x, load1(g + i), y, z, h, s);
+        p[i] = x;
+        m[i] = y;
+        v[i] = z;
+        if (t.copy) t.copy[i] = __float2bfloat16_rn(x);
+      }
+    }
+  }
+}
+
+// 8-bit moments: a warp owns the 256 elements of one scale, 4 at 4 l and 4 at
+// 128 + 4 l per lane l.
+template <typename G, int N>
+__global__ void __launch_bounds__(kThreads)
+adamw8_kernel(const __grid_constant__ AdamBatch<N> b, const AdamHyper h) {
+  __shared__ StepScalars s_step;
+  dev::pdl_trigger();
+  dev::pdl_wait();
+  if (threadIdx.x == 0) s_step = step_scalars(h);
+  __syncthreads();
+  const StepScalars s = s_step;
+  if (s.skip) {
+    if (blockIdx.x == 0 && threadIdx.x == 0 && h.status) atomicOr(h.status, MOE_STATUS_NONFINITE);
+    return;
+  }
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  for (int c = blockIdx.x; c < b.first[b.n]; c += gridDim.x) {
+    const int n = tensor_of(b, c);
+    const AdamTensor& t = b.t[n];
+    const int64_t base = static_cast<int64_t>(c - b.first[n]) * kChunk + warp * kQBlock;
+    if (base >= t.len) continue;  // the same for the whole warp
+    float* p = t.p;
+    const G* g = static_cast<const G*>(t.g);
+    uint8_t* m = static_cast<uint8_t*>(t.m);
+    uint8_t* v = static_cast<uint8_t*>(t.v);
+    const bool full = base + kQBlock <= t.len;
+    float fp[2][4], fg[2][4], fm[2][4], fr[2][4];
+    uint32_t qm[2], qv[2];
+    const float ms = t.ms[base / kQBlock], vs = t.vs[base / kQBlock];
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+      const int64_t i = base + u * 128 + lane * 4;
+      if (full) {
+        load4(p + i, fp[u]);
+        load4(g + i, fg[u]);
+        qm[u] = *reinterpret_cast<const uint32_t*>(m + i);
+        qv[u] = *reinterpret_cast<const uint32_t*>(v + i);
+      } else {
+        qm[u] = qv[u] = 0u;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const bool in = i + k < t.len;
+          fp[u][k] = in ? p[i + k] : 0.f;
+          fg[u][k] = in ? load1(g + i + k) : 0.f;
+          if (in) {
+            qm[u] |= static_cast<uint32_t>(m[i + k]) << (8 * k);
+            qv[u] |= static_cast<uint32_t>(v[i + k]) << (8 * k);
+          }
+        }
+      }
+    }
+    float top_m = 0.f, top_r = 0.f;
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+      of_e4m3x4(qm[u], fm[u]);
+      of_e4m3x4(qv[u], fr[u]);
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        fm[u][k] *= ms;
+        const float r = fr[u][k] * vs;
+        float sq = r * r;
+        fr[u][k] = adam_one(fp[u][k], fg[u][k], fm[u][k], sq, h, s);
+        top_m = fmaxf(top_m, fabsf(fm[u][k]));
+        top_r = fmaxf(top_r, fr[u][k]);
+        // fmaxf drops a NaN: it has to reach the scale
+        if (!(fabsf(fm[u][k]) < INFINITY)) top_m = INFINITY;
+        if (!(fr[u][k] < INFINITY)) top_r = INFINITY;
+      }
+    }
+    // non-negative floats keep their order as integers
+    top_m = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(top_m)));
+    top_r = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(top_r)));
+    const float sm = top_m >= kTiny ? top_m * (1.0f / 448.0f) : 0.f;
+    const float sr = top_r * (1.0f / 448.0f);
+    const float im = sm > 0.f ? 448.0f / top_m : 0.f;
+    const float ir = sr > 0.f ? 448.0f / top_r : 0.f;
+    if (lane == 0) {
+      t.ms[base / kQBlock] = sm;
+      t.vs[base / kQBlock] = sr;
+    }
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+      const int64_t i = base + u * 128 + lane * 4;
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        fm[u][k] *= im;
+        const float x = fr[u][k] * ir;
+        fr[u][k] = fr[u][k] > 0.f ? fmaxf(x, 0.001953125f) : 0.f;  // 2^-9, the smallest code
+      }
+      qm[u] = to_e4m3x4(fm[u]);
+      qv[u] = to_e4m3x4(fr[u]);
+      if (full) {
+        store4(p + i, fp[u]);
+        *reinterpret_cast<uint32_t*>(m + i) = qm[u];
+        *reinterpret_cast<uint32_t*>(v + i) = qv[u];
+        if (t.copy) store4(t.copy + i, fp[u]);
+      } else {
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          if (i + k < t.len) {
+            p[i + k] = fp[u][k];
+            m[i + k] = static_cast<uint8_t>(qm[u] >> (8 * k));
+            v[i + k] = static_cast<uint8_t>(qv[u] >> (8 * k));
+            if (t.copy) t.copy[i + k] = __float2bfloat16_rn(fp[u][k]);
+          }
+        }
+      }
+    }
+  }
+}
+
+struct Lists {
+  const int64_t* len;
+  float* const* param;
+  const void* const* grad;
+  void* const* m;
+  void* const* v;
+  float* const* ms;
+  float* const* vs;
+  void* const* copy;
+};
+
+int32_t bad_arg(const std::string& what) {
+  return fail(MOE_ERR_INVALID_ARGUMENT, "moe_adamw: " + what);
+}
+
+int32_t check_lists(const moe_adamw_config* c, int32_t n, const Lists& l) {
+  if (!c) return bad_arg("config is null");
+  if (n < 0) return bad_arg("negative tensor count");
+  if (n > kMaxTensors)
+    return fail(MOE_ERR_UNSUPPORTED, "moe_adamw: more than " + std::to_string(kMaxTensors) + " tensors");
+  if (c->grad_dtype != MOE_DTYPE_BF16 && c->grad_dtype != MOE_DTYPE_F32)
+    return bad_arg("unknown gradient dtype");
+  if (c->state_bits != 32 && c->state_bits != 8) return bad_arg("state_bits must be 32 or 8");
+  if (n > 0 && (!l.len || !l.param || !l.grad || !l.m || !l.v)) return bad_arg("null tensor array");
+  if (n > 0 && c->state_bits == 8 && (!l.ms || !l.vs)) return bad_arg("null scale array");
+  int64_t chunks = 0;
+  for (int32_t i = 0; i < n; ++i) {
+    if (l.len[i] < 0) return bad_arg("negative length");
+    if (l.len[i] == 0) continue;
+    const void* need[6] = {l.param[i], l.grad[i], l.m[i], l.v[i],
+                           c->state_bits == 8 ? l.ms[i] : l.param[i],
+                           c->state_bits == 8 ? l.vs[i] : l.param[i]};
+    for (int q = 0; q < 4; ++q) {
+      if (!need[q]) return bad_arg("null tensor");
+      if (!aligned16(need[q])) return fail(MOE_ERR_ALIGNMENT, "moe_adamw: tensor not 16-byte aligned");
+    }
+    for (int q = 4; q < 6; ++q) {
+      if (!need[q]) return bad_arg("null scales");
+      if (reinterpret_cast<uintptr_t>(need[q]) & 3u)
+        return fail(MOE_ERR_ALIGNMENT, "moe_adamw: scales not 4-byte aligned");
+    }
+    if (l.copy && l.copy[i] && !aligned16(l.copy[i]))
+      return fail(MOE_ERR_ALIGNMENT, "moe_adamw: bf16 copy not 16-byte aligned");
+    chunks += (l.len[i] + kChunk - 1) / kChunk;
+    if (chunks > 2147483647) return fail(MOE_ERR_UNSUPPORTED, "moe_adamw: more than 2^42 elements");
+  }
+  return MOE_OK;
+}
+
+int32_t check_hyper(const moe_adamw_config* c, const double* norm, const double* step_lr) {
+  auto fraction = [](double b) { return b >= 0.0 && b < 1.0; };
+  if (!fraction(c->beta1) || !fraction(c->beta2)) return bad_arg("beta outside [0, 1)");
+  // 0 / 0 for a parameter whose gradients were all zero
+  if (!(c->eps >= FLT_MIN) || !(c->eps <= FLT_MAX)) return bad_arg("eps must be a normal positive fp32 number");
+  if (!(c->weight_decay >= 0.0) || !std::isfinite(c->weight_decay))
+    return bad_arg("weight_decay must be >= 0 and finite");
+  if (!step_lr && (c->step < 1 || !std::isfinite(c->lr))) return bad_arg("step must be >= 1, lr finite");
+  if (norm && (!(c->max_norm > 0.0) || !std::isfinite(c->max_norm)))
+    return bad_arg("max_norm must be positive and finite");
+  for (const double* q : {norm, step_lr})
+    if (reinterpret_cast<uintptr_t>(q) & 7u)
+      return fail(MOE_ERR_ALIGNMENT, "moe_adamw: norm / step_lr not 8-byte aligned");
+  return MOE_OK;
+}
+
+template <typename G, int N>
+void launch_batch(const AdamBatch<N>& b, const AdamHyper& h, bool bits8, cudaStream_t s) {
+  const int chunks = b.first[b.n];
+  const int most = num_sms() * 8;
+  const dim3 grid(static_cast<unsigned>(std::min(chunks, most)));
+  if (bits8) launch_pdl(adamw8_kernel<G, N>, grid, dim3(kThreads), 0, s, b, h);
+  else launch_pdl(adamw_kernel<G, N>, grid, dim3(kThreads), 0, s, b, h);
+}
+
+template <int N>
+int32_t run_batches(const moe_adamw_config& c, int32_t n, const Lists& l, const AdamHyper& h,
+                    cudaStream_t s) {
+  AdamBatch<N> b;
+  const bool bits8 = c.state_bits == 8;
+  for (int32_t i = 0; i < n;) {
+    b.n = 0;
+    b.first[0] = 0;
+    for (; i < n && b.n < N; ++i) {
+      if (l.len[i] == 0) continue;
+      b.t[b.n] = AdamTensor{l.param[i], l.grad[i], l.m[i], l.v[i], bits8 ? l.ms[i] : nullptr,
+                            bits8 ? l.vs[i] : nullptr,
+                            l.copy ? static_cast<__nv_bfloat16*>(l.copy[i]) : nullptr, l.len[i]};
+      b.first[b.n + 1] = b.first[b.n] + static_cast<int32_t>((l.len[i] + kChunk - 1) / kChunk);
+      ++b.n;
+    }
+    if (b.n == 0) break;
+    if (c.grad_dtype == MOE_DTYPE_BF16) launch_batch<__nv_bfloat16, N>(b, h, bits8, s);
+    else launch_batch<float, N>(b, h, bits8, s);
+    const int32_t rc = check_launch("adamw_kernel");
+    if (rc != MOE_OK) return rc;
+  }
+  return MOE_OK;
+}
+
+}  // namespace
+}  // namespace moe
+
+using namespace moe;
+
+extern "C" size_t moe_adamw_config_size(void) { return sizeof(moe_adamw_config); }
+
+extern "C" int32_t moe_adamw_check(const moe_adamw_config* cfg, int32_t n, const int64_t* len,
+                                   float* const* param, const void* const* grad, void* const* m,
+                                   void* const* v, float* const* m_scale, float* const* v_scale,
+                                   void* const* bf16_copy) {
+  set_last_error("");
+  const Lists l{len, param, grad, m, v, m_scale, v_scale, bf16_copy};
+  int32_t rc = check_lists(cfg, n, l);
+  if (rc != MOE_OK) return rc;
+  // what the step writes must not overlap anything else it reads or writes
+  struct Range {
+    uintptr_t lo, hi;
+    bool written;
+  };
+  std::vector<Range> r;
+  const bool bits8 = cfg->state_bits == 8;
+  const int64_t es = bits8 ? 1 : 4;
+  auto add = [&](const void* q, int64_t bytes, bool written) {
+    if (q) r.push_back(Range{reinterpret_cast<uintptr_t>(q), reinterpret_cast<uintptr_t>(q) + bytes, written});
+  };
+  for (int32_t i = 0; i < n; ++i) {
+    if (len[i] == 0) continue;
+    add(param[i], 4 * len[i], true);
+    add(grad[i], (cfg->grad_dtype == MOE_DTYPE_BF16 ? 2 : 4) * len[i], false);
+    add(m[i], es * len[i], true);
+    add(v[i], es * len[i], true);
+    if (bits8) {
+      const int64_t blocks = (len[i] + kQBlock - 1) / kQBlock;
+      add(m_scale[i], 4 * blocks, true);
+      add(v_scale[i], 4 * blocks, true);
+    }
+    if (bf16_copy) add(bf16_copy[i], 2 * len[i], true);
+  }
+  std::sort(r.begin(), r.end(), [](const Range& a, const Range& b) { return a.lo < b.lo; });
+  uintptr_t end_any = 0, end_written = 0;
+  for (const Range& q : r) {
+    if (q.lo < (q.written ? end_any : end_written))
+      return bad_arg("a tensor that the step writes overlaps another one");
+    end_any = std::max(end_any, q.hi);
+    if (q.written) end_written = std::max(end_written, q.hi);
+  }
+  return MOE_OK;
+}
+
+extern "C" int32_t moe_adamw_step(const moe_adamw_config* cfg, int32_t n, const int64_t* len,
+                                  float* const* param, const void* const* grad, void* const* m,
+                                  void* const* v, float* const* m_scale, float* const* v_scale,
+                                  void* const* bf16_copy, const double* norm,
+                                  const double* step_lr, int32_t* status, moe_stream_t stream) {
+  CallRange range_("moe_adamw_step");
+  set_last_error("");
+  const Lists l{len, param, grad, m, v, m_scale, v_scale, bf16_copy};
+  int32_t rc = check_lists(cfg, n, l);
+  if (rc != MOE_OK) return rc;
+  rc = check_hyper(cfg, norm, step_lr);
+  if (rc != MOE_OK) return rc;
+  AdamHyper h{};
+  h.b1 = static_cast<float>(cfg->beta1);
+  h.nb1 = static_cast<float>(1.0 - cfg->beta1);
+  h.b2 = static_cast<float>(cfg->beta2);
+  h.nb2 = static_cast<float>(1.0 - cfg->beta2);
+  h.eps = static_cast<float>(cfg->eps);
+  h.lr = cfg->lr;
+  h.wd = cfg->weight_decay;
+  h.step = static_cast<double>(cfg->step);
+  h.beta1 = cfg->beta1;
+  h.beta2 = cfg->beta2;
+  h.max_norm = cfg->max_norm;
+  h.norm = norm;
+  h.step_lr = step_lr;
+  h.status = status;
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  if (n <= kSmallBatch) return run_batches<kSmallBatch>(*cfg, n, l, h, s);
+  return run_batches<kLargeBatch>(*cfg, n, l, h, s);
+}

@@ -125,6 +125,25 @@ int32_t launch_aux_loss(const moe_config& c, const float* logits, double alpha, 
 int32_t launch_combine(const moe_config& c, const void* ye, const int32_t* expert_idx,
                        const float* gate, const int32_t* slot, const uint8_t* kept, void* y,
                        int32_t* status, cudaStream_t s);
+// routing by scores and its gradient (route_scores.cu)
+int32_t launch_route(const moe_route_config& c, const void* logits, const float* bias,
+                     int32_t* expert_idx, float* gate, int32_t* status, cudaStream_t s);
+int32_t launch_route_backward(const moe_route_config& c, const void* logits,
+                              const int32_t* expert_idx, const float* dgate, void* dlogits,
+                              int32_t* status, cudaStream_t s);
+// the row exchange for up to kMaxChoices choices a token (choices.cu)
+constexpr int kMaxChoices = 16;
+int32_t launch_scatter_choices(const moe_config& c, const void* x, const int32_t* expert_idx,
+                               const int32_t* slot, const uint8_t* kept, void* xe, int32_t* status,
+                               cudaStream_t s);
+// out[t] = sum over kept choices of gate * rows (gate null: 1)
+int32_t launch_gather_choices(const moe_config& c, const void* rows, const int32_t* expert_idx,
+                              const float* gate, const int32_t* slot, const uint8_t* kept,
+                              void* out, int32_t* status, cudaStream_t s);
+int32_t launch_combine_backward(const moe_config& c, const void* dy, const void* ye,
+                                const int32_t* expert_idx, const float* gate, const int32_t* slot,
+                                const uint8_t* kept, void* dye, float* dgate, int32_t* status,
+                                cudaStream_t s);
 // expert parallelism over the ranks of one node: the receive buffers of all
 // ranks as mapped into this process, rank order
 constexpr int kMaxEpRanks = 8;

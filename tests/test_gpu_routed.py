@@ -1,0 +1,617 @@
+"""Routing by scores and the row exchange for up to 16 choices a token, forward and backward,
+against 64-bit statements (tests/routed_ref.py).
+
+Tolerances.  u = 2^-24 is half a step of fp32, h = 2^-8 of bf16 (finfo.eps / 2).
+ * gates: the logit difference in the exponent is off by |x - m| u <= 32 u for the inputs here,
+   expf by 4 u, a sum of at most 256 terms (8 per lane, 5 shuffles) by 13 u, a division and two
+   products by 3 u, and for renormalised sigmoids two such quotients: under 128 u relative.
+ * dlogits: a product of up to three such factors with a difference a - dot, where dot (16 terms)
+   is off by its terms' magnitudes: 512 u of (|a| + sum |a_i s_i|) s.  bf16: plus h of the value.
+ * gathered rows: k terms in order, k u of the sum of magnitudes, plus h (bf16) or u (fp32) of
+   the result.  dgate: a row of d products: (d / 32 + 16) u of the sum of magnitudes.
+"""
+import math
+
+import pytest
+import torch
+
+import routed_ref as ref
+
+pytestmark = pytest.mark.gpu
+
+U, H = 2.0 ** -24, 2.0 ** -8
+DTYPES = [torch.float32, torch.bfloat16]
+
+
+@pytest.fixture(scope="module")
+def moe(cuda_device):
+    import sparse_mixture_experts_fwd_b200 as m
+    return m
+
+
+def half_step(dtype):
+    return torch.finfo(dtype).eps / 2
+
+
+def status_word():
+    return torch.zeros(1, dtype=torch.int32, device="cuda")
+
+
+def check_route(moe, x, k, bias=None, want_status=0, **kw):
+    """Choices equal, gates within 128 u; canaries behind the outputs untouched."""
+    T, E = x.shape
+    dev = "cuda"
+    names = dict(groups="num_groups")
+    cfg = moe.make_route_config(T, E, k, dtype=x.dtype,
+                                **{names.get(n, n): v for n, v in kw.items()})
+    idx = torch.full((T + 1, k), -77, dtype=torch.int32, device=dev)
+    gate = torch.full((T + 1, k), -77.0, device=dev)
+    st = status_word()
+    moe.route(cfg, x.to(dev), None if bias is None else bias.to(dev), expert_idx=idx[:T],
+              gate=gate[:T], status=st)
+    ri, rw = ref.route(x, k, bias=bias, **kw)
+    assert int(st) == want_status
+    assert bool((idx[T] == -77).all()) and bool((gate[T] == -77).all())
+    assert torch.equal(idx[:T].cpu(), ri)
+    err = (gate[:T].cpu().double() - rw).abs()
+    assert bool((err <= 128 * U * rw.abs() + 1e-37).all()), float(err.max())
+    return idx[:T], gate[:T]
+
+
+SHAPES = [
+    # T, E, k, groups, top_groups, group_top
+    (1, 1, 1, 1, 1, 1), (3, 2, 2, 1, 1, 1), (17, 8, 3, 1, 1, 1), (65, 60, 6, 1, 1, 1),
+    (33, 64, 8, 8, 3, 2), (129, 256, 8, 8, 4, 2), (40, 256, 16, 1, 1, 1), (50, 255, 5, 5, 2, 2),
+    (41, 240, 7, 15, 4, 1), (37, 100, 16, 4, 2, 2), (29, 96, 4, 32, 9, 2), (31, 252, 9, 9, 3, 2),
+    (23, 37, 2, 1, 1, 1), (1200, 128, 4, 2, 1, 1), (19, 12, 4, 3, 2, 1), (64, 129, 16, 3, 3, 2),
+]
+
+
+@pytest.mark.parametrize("dtype", DTYPES, ids=["f32", "bf16"])
+@pytest.mark.parametrize("shape", SHAPES, ids=[str(s) for s in SHAPES])
+def test_route_shapes(moe, shape, dtype):
+    T, E, k, G, tg, gt = shape
+    g = torch.Generator().manual_seed(T * 1000 + E)
+    x = (1.5 * torch.randn(T, E, generator=g)).to(dtype)
+    b = 0.1 * torch.randn(E, generator=g)
+    for score in ("softmax", "sigmoid"):
+        for renorm in (False, True):
+            for bias in (None, b):
+                check_route(moe, x, k, bias, score=score, renorm=renorm, groups=G, top_groups=tg,
+                            group_top=gt, scale=2.5 if renorm else 1.0)
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+def test_route_equal_candidates(moe, score):
+    """All logits equal: the lowest experts of the lowest groups, in order."""
+    x = torch.full((5, 64), 0.75)
+    b = torch.full((64,), 0.01)
+    for bias in (None, b):
+        idx, _ = check_route(moe, x, 6, bias, score=score)
+        assert idx[0].tolist() == [0, 1, 2, 3, 4, 5]
+        idx, _ = check_route(moe, x, 12, bias, score=score, groups=8, top_groups=2, group_top=2)
+        assert idx[0].tolist() == list(range(12))
+    # zeros of both signs are equal
+    z = torch.zeros(3, 16)
+    z[:, ::2] = -0.0
+    for dt in DTYPES:
+        idx, _ = check_route(moe, z.to(dt), 4, score=score)
+        assert idx[0].tolist() == [0, 1, 2, 3]
+
+
+@pytest.mark.parametrize("bias_on", [False, True])
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+def test_route_candidates_one_step_apart(moe, score, bias_on):
+    """Logits whose scores fp32 cannot tell apart: neighbours in fp32 around one value, shuffled,
+    the order is the exact one; the same across the border of the top groups."""
+    g = torch.Generator().manual_seed(4)
+    E, T = 64, 48
+    base = torch.tensor([0.5, 2.0, 7.0, -3.0]).repeat(T // 4)[:, None]
+    x = base.clone().expand(T, E).contiguous()
+    bits = x.view(torch.int32) + torch.stack([torch.randperm(E, generator=g) for _ in range(T)]).int()
+    x = bits.view(torch.float32)
+    b = torch.full((E,), 0.03125) if bias_on else None
+    check_route(moe, x, 7, b, score=score)
+    check_route(moe, x, 5, b, score=score, groups=8, top_groups=3, group_top=2)
+    check_route(moe, x, 5, b, score=score, groups=8, top_groups=3, group_top=1)
+    # equal pairs at the border, with a third candidate one step above them
+    y = torch.full((T, 16), -1.0)
+    y[:, 3] = y[:, 9] = 1.0
+    y[:, 12] = torch.nextafter(torch.tensor(1.0), torch.tensor(2.0))
+    check_route(moe, y, 1, None if b is None else b[:16], score=score)
+    check_route(moe, y, 2, None if b is None else b[:16], score=score)
+
+
+def test_route_border_hidden_behind_equal_ones(moe):
+    """Many exactly equal candidates at the last place, and one that differs from them by less
+    than fp32 shows (its bias makes up for a smaller logit)."""
+    E, k = 32, 4
+    x = torch.full((8, E), 0.25)
+    b = torch.full((E,), 0.5)
+    x[:, 20] = 0.25 + 2.0 ** -20
+    b[20] = 0.5 - 2.0 ** -23
+    for t in range(8):
+        x[t, :t] += 1.0
+    check_route(moe, x, k, b, score="sigmoid")
+    check_route(moe, x, k, b, score="softmax")
+
+
+@pytest.mark.parametrize("dtype", DTYPES, ids=["f32", "bf16"])
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+def test_route_masks(moe, score, dtype):
+    g = torch.Generator().manual_seed(9)
+    T, E, k = 40, 48, 6
+    x = torch.randn(T, E, generator=g).to(dtype)
+    x[3] = -math.inf                                # nothing left
+    x[4] = torch.finfo(dtype).min                   # the same by the type's lowest value
+    x[5, 2:] = -math.inf                            # two left of six
+    x[6, 1:] = torch.finfo(torch.bfloat16).min
+    x[7, 5:] = -math.inf
+    x[7, 0] = 3.0e4                                 # a large logit among few
+    x[8, :] = -200.0                                # scores that underflow in fp32
+    x[8, 11] = -190.0
+    b = 0.2 * torch.randn(E, generator=g)
+    bm = b.clone()
+    bm[10:20] = -math.inf
+    for bias in (None, b, bm):
+        for renorm in (False, True):
+            idx, gate = check_route(moe, x, k, bias, score=score, renorm=renorm)
+            assert idx[3].tolist() == [-1] * k == idx[4].tolist() and float(gate[3].abs().sum()) == 0
+            check_route(moe, x, k, bias, score=score, renorm=renorm, groups=4, top_groups=2,
+                        group_top=2)
+            check_route(moe, x, 3, bias, score=score, renorm=renorm, groups=4, top_groups=1,
+                        group_top=1)
+    idx, _ = check_route(moe, x, k, bm, score=score)
+    assert not bool(((idx >= 10) & (idx < 20)).any())
+
+
+@pytest.mark.parametrize("dtype", DTYPES, ids=["f32", "bf16"])
+def test_route_nan_and_inf_are_masked_and_reported(moe, dtype):
+    g = torch.Generator().manual_seed(1)
+    x = torch.randn(20, 24, generator=g).to(dtype)
+    for t, v in ((0, math.nan), (7, math.inf)):
+        y = x.clone()
+        y[t, 5] = v
+        idx, _ = check_route(moe, y, 4, want_status=moe.STATUS_BAD_LOGIT, score="softmax")
+        assert not bool((idx[t] == 5).any())
+    for v in (math.nan, math.inf):
+        b = torch.zeros(24)
+        b[9] = v
+        idx, _ = check_route(moe, x, 4, b, want_status=moe.STATUS_BAD_LOGIT, score="sigmoid")
+        assert not bool((idx == 9).any())
+
+
+def test_route_wide_ranges(moe):
+    """Saturated sigmoids, peaked softmaxes and large biases: fp64 still decides rightly."""
+    g = torch.Generator().manual_seed(2)
+    x = 12.0 * torch.randn(300, 64, generator=g)
+    b = torch.randn(64, generator=g)
+    # without a bias the logits decide; with one, sums that fp64 rounds to the same value are
+    # ties in the reference too
+    for score in ("softmax", "sigmoid"):
+        check_route(moe, x.clamp(-30, 30), 8, score=score)
+        check_route(moe, x.clamp(-30, 30), 8, score=score, renorm=True)
+        check_route(moe, x.clamp(-15, 15), 8, b, score=score)
+        check_route(moe, x.clamp(-15, 15), 8, 1e4 * b, score=score)
+
+
+def test_route_empty_batch_and_refusals(moe):
+    cfg = moe.make_route_config(0, 16, 4)
+    idx, gate = moe.route(cfg, torch.empty(0, 16, device="cuda"))
+    assert idx.shape == (0, 4) and gate.shape == (0, 4)
+    cfg = moe.make_route_config(4, 16, 4)
+    x = torch.zeros(4, 16, device="cuda")
+    with pytest.raises(TypeError, match="logits"):
+        moe.route(cfg, x.bfloat16())
+    with pytest.raises(ValueError, match="shape"):
+        moe.route(cfg, x[:3])
+    with pytest.raises(ValueError, match="contiguous"):
+        moe.route(cfg, torch.zeros(16, 4, device="cuda").t())
+    with pytest.raises(TypeError, match="bias"):
+        moe.route(cfg, x, torch.zeros(16, device="cuda", dtype=torch.float64))
+    with pytest.raises(moe.MoEError, match="aligned"):
+        moe.route(cfg, torch.zeros(65, device="cuda")[1:].view(4, 16))
+
+
+def check_route_backward(moe, x, idx, dgate, want_status=0, **kw):
+    T, E = x.shape
+    k = idx.shape[1]
+    cfg = moe.make_route_config(T, E, k, dtype=x.dtype, **kw)
+    out = torch.full((T + 1, E), -77.0, dtype=x.dtype, device="cuda")
+    st = status_word()
+    moe.route_backward(cfg, x.cuda(), idx.cuda(), dgate.cuda(), dlogits=out[:T], status=st)
+    assert int(st) == want_status
+    assert bool((out[T] == -77).all())
+    return out[:T].cpu().double()
+
+
+def backward_bound(x, idx, dgate, want, **kw):
+    s, _ = ref.scores(x, kw.get("score", "softmax"))
+    a = (kw.get("scale", 1.0) * dgate.double()).abs()
+    w = ref.gates(x.double(), idx, score=kw.get("score", "softmax"), renorm=kw.get("renorm", False))
+    per = (a * w.abs()).sum(1, keepdim=True)
+    if kw.get("renorm"):
+        size = torch.zeros_like(s).scatter_add_(
+            1, idx.clamp(min=0).long(), torch.where(idx >= 0, w.abs() * (a + per), 0.0))
+    elif kw.get("score") == "sigmoid":
+        size = torch.zeros_like(s).scatter_add_(
+            1, idx.clamp(min=0).long(), torch.where(idx >= 0, w.abs() * a, 0.0))
+    else:
+        full = torch.zeros_like(s).scatter_add_(1, idx.clamp(min=0).long(),
+                                                torch.where(idx >= 0, a, 0.0))
+        size = s * (full + per)
+    h = H if x.dtype == torch.bfloat16 else U
+    # The reference's own rounding: autograd forms an entry that is exactly 0 (an expert that was
+    # not chosen, renormalised) as s (ds - sum ds s) from terms of up to sum |a|, each off by a
+    # few 2^-53, over at most 256 summands; 512 * 2^-53 of them covers it.
+    own = 512 * 2.0 ** -53 * a.sum(1, keepdim=True)
+    return 512 * U * size + h * want.abs() + own + 1e-37
+
+
+@pytest.mark.parametrize("dtype", DTYPES, ids=["f32", "bf16"])
+@pytest.mark.parametrize("renorm", [False, True])
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+def test_route_backward(moe, score, renorm, dtype):
+    for T, E, k in [(1, 1, 1), (5, 2, 2), (33, 60, 6), (130, 256, 8), (21, 255, 16), (700, 64, 5),
+                    (9, 37, 3)]:
+        g = torch.Generator().manual_seed(T + E)
+        x = (1.5 * torch.randn(T, E, generator=g)).to(dtype)
+        if T > 8:
+            x[2] = -math.inf
+            x[4, 1:] = torch.finfo(dtype).min
+            x[5, ::2] = -math.inf
+        kw = dict(score=score, renorm=renorm, scale=1.75)
+        idx, _ = ref.route(x, k, **kw)
+        dgate = torch.randn(T, k, generator=g)
+        want = ref.route_backward(x, idx, dgate, **kw)
+        got = check_route_backward(moe, x, idx, dgate, **kw)
+        err = (got - want).abs()
+        assert bool((err <= backward_bound(x, idx, dgate, want, **kw)).all()), float(err.max())
+
+
+@pytest.mark.parametrize("renorm", [False, True])
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+def test_route_backward_against_differences(moe, score, renorm):
+    """Central differences of the 64-bit weights: step 1e-5, truncation about 1e-10, and the
+    fp32 kernel's own 512 u of values near 1."""
+    g = torch.Generator().manual_seed(3)
+    T, E, k, eps = 6, 12, 4, 1e-5
+    x = torch.randn(T, E, generator=g)
+    kw = dict(score=score, renorm=renorm, scale=1.25)
+    idx, _ = ref.route(x, k, **kw)
+    dgate = torch.randn(T, k, generator=g)
+    got = check_route_backward(moe, x, idx, dgate, **kw)
+    for e in range(E):
+        d = torch.zeros(T, E, dtype=torch.float64)
+        d[:, e] = eps
+        up, down = (ref.gates(x.double() + f * d, idx, **kw) for f in (1, -1))
+        diff = ((up - down) * dgate.double()).sum(1) / (2 * eps)
+        assert bool(((got[:, e] - diff).abs() <= 1e-8 + 512 * U * 4).all())
+
+
+def test_route_backward_repeated_and_bad_choices(moe):
+    g = torch.Generator().manual_seed(5)
+    T, E, k = 9, 20, 4
+    x = torch.randn(T, E, generator=g)
+    idx = torch.randint(0, E, (T, k), generator=g, dtype=torch.int32)
+    idx[0] = 7                 # the same expert four times
+    idx[1, 2] = -1             # not a choice
+    idx[2, :2] = 3
+    dgate = torch.randn(T, k, generator=g)
+    for score in ("softmax", "sigmoid"):
+        for renorm in (False, True):
+            kw = dict(score=score, renorm=renorm)
+            want = ref.route_backward(x, idx, dgate, **kw)
+            got = check_route_backward(moe, x, idx, dgate, **kw)
+            assert bool(((got - want).abs() <= backward_bound(x, idx, dgate, want, **kw)).all())
+    bad = idx.clone()
+    bad[4, 1], bad[5, 0] = E, -5
+    good = bad.clone()
+    good[4, 1] = good[5, 0] = -1
+    got = check_route_backward(moe, x, bad, dgate, want_status=moe.STATUS_BAD_INDEX)
+    assert torch.equal(got, check_route_backward(moe, x, good, dgate))
+
+
+# ---- the row exchange -------------------------------------------------------------
+
+
+def choices(T, E, k, seed, share_missing=0.0):
+    g = torch.Generator().manual_seed(seed)
+    liking = torch.rand(T, E, generator=g) + 0.4 * torch.rand(E, generator=g)
+    idx = liking.argsort(dim=1, descending=True)[:, :k].to(torch.int32).contiguous()
+    if share_missing:
+        idx[torch.rand(T, k, generator=g) < share_missing] = -1
+    return idx
+
+
+ROWS = [
+    # T, E, k, C, d
+    (1, 4, 3, 1, 64), (5, 128, 4, 5, 768), (37, 16, 8, 20, 128), (300, 9, 5, 100, 192),
+    (64, 256, 16, 3, 64), (2000, 32, 3, 150, 64), (11, 3, 1, 4, 320), (50, 8, 2, 9, 2560),
+    (400, 40, 9, 90, 64), (7, 16, 16, 0, 64),
+]
+
+
+@pytest.mark.parametrize("case", ROWS, ids=[str(c) for c in ROWS])
+def test_assign(moe, case):
+    T, E, k, C, d = case
+    idx = choices(T, E, k, T + E, 0.1)
+    cfg = moe.make_config(T, d, 64, E, k, C)
+    got = moe.assign(cfg, idx.cuda())
+    want = ref.assign(idx, E, C)
+    for name, v in want.items():
+        assert torch.equal(got[name].cpu(), v), name
+
+
+def test_assign_many_choices(moe):
+    """More choices than the assignment holds in registers (its second walk)."""
+    T, E, k, C = 40000, 64, 8, 4000
+    idx = choices(T, E, k, 1, 0.02)
+    got = moe.assign(moe.make_config(T, 64, 64, E, k, C), idx.cuda())
+    e = idx.reshape(-1).long()
+    there = e >= 0
+    order = torch.argsort(torch.where(there, e, E), stable=True)
+    arrivals = torch.bincount(e[there], minlength=E)
+    first = torch.cat([torch.zeros(1, dtype=torch.long), arrivals.cumsum(0)[:-1]])
+    slot = torch.full((T * k,), 2 ** 31 - 1)
+    n = int(there.sum())
+    slot[order[:n]] = torch.arange(n) - first[e[order[:n]]]
+    assert torch.equal(got["slot"].cpu().view(-1).long(), slot)
+    assert torch.equal(got["arrivals"].cpu().long(), arrivals)
+    assert torch.equal(got["kept"].cpu().view(-1).bool(), there & (slot < C))
+    assert int(got["n_dropped"]) == int((arrivals - C).clamp(min=0).sum())
+
+
+def exchange(case, dtype, seed=0):
+    T, E, k, C, d = case
+    g = torch.Generator().manual_seed(seed + T)
+    idx = choices(T, E, k, T + E, 0.05)
+    a = ref.assign(idx, E, C)
+    x = torch.randn(T, d, generator=g).to(dtype)
+    rows = torch.randn(E, C, d, generator=g).to(dtype)
+    gate = torch.rand(T, k, generator=g)
+    return idx, a["slot"], a["kept"], x, rows, gate
+
+
+@pytest.mark.parametrize("dtype", DTYPES, ids=["f32", "bf16"])
+@pytest.mark.parametrize("case", ROWS, ids=[str(c) for c in ROWS])
+def test_row_exchange(moe, case, dtype):
+    T, E, k, C, d = case
+    idx, slot, kept, x, rows, gate = exchange(case, dtype)
+    cfg = moe.make_config(T, d, 64, E, k, C, dtype=dtype)
+    D = [t.cuda() for t in (idx, slot, kept)]
+    h = half_step(dtype)
+    P = 2
+    # dispatch: the kept rows, canaries elsewhere
+    big = torch.full((E * C + 2 * P, d), -7.0, dtype=dtype, device="cuda")
+    moe.dispatch(cfg, x.cuda(), *D, xe=big[P:P + E * C].view(E, C, d))
+    want = torch.full((E * C + 2 * P, d), -7.0, dtype=dtype)
+    t, j, r = ref.rows_of(idx, slot, kept, C)
+    want[P + r] = x[t]
+    assert torch.equal(big.cpu(), want)
+    # combine and dispatch's gradient
+    out = torch.full((T + 1, d), -7.0, dtype=dtype, device="cuda")
+    for w in (gate, None):
+        if w is not None:
+            moe.combine(cfg, rows.cuda(), D[0], w.cuda(), D[1], D[2], y=out[:T])
+        else:
+            moe.dispatch_backward(cfg, rows.cuda(), *D, dx=out[:T])
+        exact = ref.gather(rows, idx, slot, kept, w)
+        size = ref.gather(rows.abs(), idx, slot, kept, w)
+        err = (out[:T].cpu().double() - exact).abs()
+        assert bool((err <= k * U * size + h * (exact.abs() + k * U * size)).all()), float(err.max())
+        assert bool((out[T] == -7).all())
+    # combine's gradient
+    dye = torch.full((E * C + 2 * P, d), -7.0, dtype=dtype, device="cuda")
+    dgate = torch.full((T + 1, k), -7.0, device="cuda")
+    moe.combine_backward(cfg, x.cuda(), rows.cuda(), D[0], gate.cuda(), D[1], D[2],
+                         dye=dye[P:P + E * C].view(E, C, d), dgate=dgate[:T])
+    rdye, rdg = ref.combine_backward(x, rows, idx, gate, slot, kept)
+    got = dye.cpu().double()
+    full = torch.full((E * C + 2 * P, d), -7.0, dtype=torch.float64)
+    full[P + r] = rdye.view(-1, d)[r]
+    # a product rounded to fp32, then to the type
+    assert bool(((got - full).abs() <= (h + U) * full.abs()).all())
+    _, mag = ref.combine_backward(x.abs(), rows.abs(), idx, gate, slot, kept)
+    assert bool(((dgate[:T].cpu().double() - rdg).abs() <= (d / 32 + 16) * U * mag).all())
+    assert bool((dgate[T] == -7).all())
+
+
+def test_combine_backward_in_place(moe):
+    case = (37, 16, 8, 20, 128)
+    T, E, k, C, d = case
+    idx, slot, kept, x, rows, gate = exchange(case, torch.bfloat16, 1)
+    cfg = moe.make_config(T, d, 64, E, k, C)
+    args = [t.cuda() for t in (idx, gate, slot, kept)]
+    ye = rows.cuda()
+    dye, dg = moe.combine_backward(cfg, x.cuda(), ye.clone(), *args, dye=ye.clone())
+    same, dg2 = moe.combine_backward(cfg, x.cuda(), ye, *args, dye=ye)
+    assert same is ye and torch.equal(same, dye) and torch.equal(dg, dg2)
+
+
+def test_combine_gradients_against_differences(moe):
+    """The loss <dy, combine(ye, gate)> is linear in both: its change along one weight and along
+    one row equals the gradient's entry (fp32 rows, relative 1e-4 of the terms' size)."""
+    case = (9, 5, 3, 4, 64)
+    T, E, k, C, d = case
+    idx, slot, kept, dy, ye, gate = exchange(case, torch.float32, 2)
+    cfg = moe.make_config(T, d, 64, E, k, C, dtype=torch.float32)
+    i, s, kp = idx.cuda(), slot.cuda(), kept.cuda()
+    dye, dgate = moe.combine_backward(cfg, dy.cuda(), ye.cuda(), i, gate.cuda(), s, kp,
+                                      dye=torch.zeros_like(ye).cuda())
+
+    def loss(y_, g_):
+        y = moe.combine(cfg, y_.cuda(), i, g_.cuda(), s, kp)
+        return float((y.cpu().double() * dy.double()).sum())
+
+    base = loss(ye, gate)
+    t, j, r = ref.rows_of(idx, slot, kept, C)
+    for n in range(0, len(t), 3):
+        g2 = gate.clone()
+        g2[t[n], j[n]] += 1.0
+        assert abs(loss(ye, g2) - base - float(dgate[t[n], j[n]])) < 1e-4 * d
+        y2 = ye.clone()
+        y2.view(-1, d)[r[n], 5] += 1.0
+        assert abs(loss(y2, gate) - base - float(dye.view(-1, d)[r[n], 5])) < 1e-4 * d
+
+
+def test_whole_layer_with_eight_choices(moe):
+    """Router logits, scored routing, slots, dispatch, the expert FFN, combine; then the gradients
+    of the weights, of the expert rows, of the logits and of the dispatched rows."""
+    g = torch.Generator().manual_seed(6)
+    T, d, f, E, k, C = 260, 128, 192, 32, 8, 80
+    x = torch.randn(T, d, generator=g).bfloat16()
+    Wr = (torch.randn(E, d, generator=g) / math.sqrt(d)).bfloat16()
+    W1 = (0.05 * torch.randn(E, f, d, generator=g)).bfloat16()
+    W2 = (0.05 * torch.randn(E, d, f, generator=g)).bfloat16()
+    b = 0.05 * torch.randn(E, generator=g)
+    cfg = moe.make_config(T, d, f, E, k, C)
+    ffn = moe.ep_ffn_config(cfg, 1)
+    rcfg = moe.make_route_config(T, E, k, score="sigmoid", num_groups=4, top_groups=2, group_top=2,
+                                 renorm=True, scale=2.5)
+    st = status_word()
+    logits = moe.router(ffn, x.cuda(), Wr.cuda(), status=st)
+    idx, gate = moe.route(rcfg, logits, b.cuda(), status=st)
+    a = moe.assign(cfg, idx, status=st)
+    xe = moe.dispatch(cfg, x.cuda(), idx, a["slot"], a["kept"], status=st)
+    _, ye = moe.expert_ffn(ffn, xe, W1.cuda(), W2.cuda(), a["kept_cnt"], status=st)
+    y = moe.combine(cfg, ye, idx, gate, a["slot"], a["kept"], status=st)
+    torch.cuda.synchronize()
+    assert int(st) == 0
+    # from the same logits, one expert after the other in 64 bits with H rounded to bf16
+    ri, rw = ref.route(logits.cpu(), k, score="sigmoid", groups=4, top_groups=2, group_top=2,
+                       renorm=True, scale=2.5, bias=b)
+    assert torch.equal(idx.cpu(), ri)
+    ra = ref.assign(ri, E, C)
+    want = torch.zeros(T, d, dtype=torch.float64)
+    for e in range(E):
+        Hx = torch.relu(x.double() @ W1[e].double().t()).bfloat16().double()
+        o = (Hx @ W2[e].double().t()).bfloat16().double()
+        m = (ri == e) & (ra["kept"] != 0)
+        want += (rw * m).sum(1, keepdim=True) * o
+    err = (y.cpu().double() - want).abs()
+    assert bool((err <= 2e-2 + 1e-2 * want.abs()).all()), float(err.max())
+    # backward
+    dy = torch.randn(T, d, generator=g).bfloat16()
+    dye, dgate = moe.combine_backward(cfg, dy.cuda(), ye, idx, gate, a["slot"], a["kept"])
+    dlogits = moe.route_backward(rcfg, logits, idx, dgate)
+    dx = moe.dispatch_backward(cfg, dye, idx, a["slot"], a["kept"])
+    filled = torch.zeros(E * C, dtype=torch.bool)
+    filled[ref.rows_of(ri, ra["slot"], ra["kept"], C)[2]] = True
+    yec = torch.where(filled.view(E, C, 1), ye.cpu(), torch.zeros((), dtype=torch.bfloat16))
+    rdye, rdg = ref.combine_backward(dy, yec, ri, gate.cpu(), ra["slot"], ra["kept"])
+    assert bool(((dye.cpu().double() - rdye).abs() <= (H + U) * rdye.abs()).all())
+    _, mag = ref.combine_backward(dy.abs(), yec.abs(), ri, gate.cpu(), ra["slot"], ra["kept"])
+    assert bool(((dgate.cpu().double() - rdg).abs() <= (d / 32 + 16) * U * mag).all())
+    kw = dict(score="sigmoid", renorm=True, scale=2.5)
+    dg = dgate.cpu()
+    want = ref.route_backward(logits.cpu(), ri, dg, **kw)
+    err = (dlogits.cpu().double() - want).abs()
+    assert bool((err <= backward_bound(logits.cpu(), ri, dg, want, **kw)).all())
+    dyc = dye.cpu()
+    want = ref.gather(dyc, ri, ra["slot"], ra["kept"])
+    size = ref.gather(dyc.abs(), ri, ra["slot"], ra["kept"])
+    assert bool(((dx.cpu().double() - want).abs() <= k * U * size + H * (want.abs() + k * U * size)).all())
+
+
+def test_streams_and_graph(moe):
+    """The chain on a side stream, and captured and replayed with new contents, gives the eager
+    call's bits."""
+    g = torch.Generator().manual_seed(8)
+    T, d, E, k, C = 90, 64, 32, 8, 40
+    cfg = moe.make_config(T, d, 64, E, k, C)
+    rcfg = moe.make_route_config(T, E, k, score="sigmoid", num_groups=4, top_groups=2, group_top=2,
+                                 renorm=True)
+    logits = torch.randn(T, E, generator=g).cuda()
+    b = (0.1 * torch.randn(E, generator=g)).cuda()
+    x = torch.randn(T, d, generator=g).bfloat16().cuda()
+    dy = torch.randn(T, d, generator=g).bfloat16().cuda()
+    o = dict(idx=torch.empty(T, k, dtype=torch.int32, device="cuda"),
+             gate=torch.empty(T, k, device="cuda"), a={},
+             xe=torch.zeros(E, C, d, dtype=torch.bfloat16, device="cuda"),
+             y=torch.empty(T, d, dtype=torch.bfloat16, device="cuda"),
+             dye=torch.zeros(E, C, d, dtype=torch.bfloat16, device="cuda"),
+             dgate=torch.empty(T, k, device="cuda"), dl=torch.empty(T, E, device="cuda"),
+             dx=torch.empty(T, d, dtype=torch.bfloat16, device="cuda"))
+
+    def chain(stream):
+        kw = dict(stream=stream)
+        moe.route(rcfg, logits, b, expert_idx=o["idx"], gate=o["gate"], **kw)
+        moe.assign(cfg, o["idx"], out=o["a"], **kw)
+        s, kp = o["a"]["slot"], o["a"]["kept"]
+        moe.dispatch(cfg, x, o["idx"], s, kp, xe=o["xe"], **kw)
+        moe.combine(cfg, o["xe"], o["idx"], o["gate"], s, kp, y=o["y"], **kw)
+        moe.combine_backward(cfg, dy, o["xe"], o["idx"], o["gate"], s, kp, dye=o["dye"],
+                             dgate=o["dgate"], **kw)
+        moe.route_backward(rcfg, logits, o["idx"], o["dgate"], dlogits=o["dl"], **kw)
+        moe.dispatch_backward(cfg, o["dye"], o["idx"], s, kp, dx=o["dx"], **kw)
+
+    def results():
+        torch.cuda.synchronize()
+        return [t.clone() for t in (o["idx"], o["gate"], o["y"], o["dgate"], o["dl"], o["dx"],
+                                    o["a"]["slot"])]
+
+    def clear():
+        for n in ("gate", "y", "dgate", "dl", "dx"):
+            o[n].fill_(float("nan"))
+        torch.cuda.synchronize()
+
+    chain(None)
+    eager = results()
+    side = torch.cuda.Stream()
+    clear()
+    chain(side)
+    assert all(torch.equal(p, q) for p, q in zip(eager, results()))
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=side, capture_error_mode="global"):
+        chain(side)
+    clear()
+    graph.replay()
+    assert all(torch.equal(p, q) for p, q in zip(eager, results()))
+    logits.copy_(torch.randn(T, E, generator=g))
+    x.copy_(torch.randn(T, d, generator=g))
+    o["xe"].zero_()
+    o["dye"].zero_()
+    chain(None)
+    eager2 = results()
+    assert not torch.equal(eager[1], eager2[1])
+    clear()
+    graph.replay()
+    assert all(torch.equal(p, q) for p, q in zip(eager2, results()))
+    del graph
+
+
+def test_two_streams_at_once(moe):
+    """Calls in flight on two streams share nothing."""
+    g = torch.Generator().manual_seed(10)
+    T, E, k = 20000, 256, 8
+    rcfg = moe.make_route_config(T, E, k, score="sigmoid", num_groups=8, top_groups=4, group_top=2)
+    xs = [torch.randn(T, E, generator=g).cuda() for _ in range(2)]
+    b = (0.1 * torch.randn(E, generator=g)).cuda()
+    alone = [moe.route(rcfg, x, b) for x in xs]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    got = [[], []]
+    for _ in range(4):
+        for n in range(2):
+            got[n].append(moe.route(rcfg, xs[n], b, stream=streams[n]))
+    torch.cuda.synchronize()
+    for n in range(2):
+        for idx, gate in got[n]:
+            assert torch.equal(idx, alone[n][0]) and torch.equal(gate, alone[n][1])
+
+
+def test_route_offsets_past_32_bits(moe):
+    """Rows whose element offset passes 2^31: the last tokens come out as they do alone."""
+    T, E, k = 2 ** 23 + 40, 256, 1
+    x = torch.zeros(T, E, dtype=torch.bfloat16, device="cuda")  # 4.3 GB
+    tail = torch.randn(64, E, generator=torch.Generator().manual_seed(1)).bfloat16().cuda()
+    x[-64:] = tail
+    cfg = moe.make_route_config(T, E, k, dtype=torch.bfloat16)
+    idx, gate = moe.route(cfg, x)
+    one = moe.make_route_config(64, E, k, dtype=torch.bfloat16)
+    ti, tg = moe.route(one, tail.contiguous())
+    assert torch.equal(idx[-64:], ti) and torch.equal(gate[-64:], tg)
+    assert int(idx[:-64].abs().max()) == 0
+    d = moe.route_backward(cfg, x, idx, gate)
+    assert torch.equal(d[-64:], moe.route_backward(one, tail, ti, tg))
