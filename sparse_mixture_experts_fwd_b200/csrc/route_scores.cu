@@ -10,6 +10,8 @@
 // The order is that of the real numbers, not of their fp32 roundings: without
 // a bias it is the logits' own order, and where fp32 cannot tell two
 // candidates apart the token is decided again in fp64 (route_exact).
+#include <cfloat>
+#include <climits>
 #include <cmath>
 
 #include "moe_internal.cuh"
@@ -19,13 +21,24 @@ namespace {
 
 constexpr unsigned kFull = 0xffffffffu;
 constexpr int kWarps = 8;  // warps per block, a token each
+constexpr int kMaxOpen = 512;  // tokens a block lists for its fp64 pass
+constexpr int32_t kOpenMark = INT_MIN;  // in expert_idx until then: one that did not fit the list
 // A logit at or below bf16's lowest value masks its expert, as -inf does.
 constexpr float kLowest = -3.3895313892515355e38f;
-// Key units (see make_key) within which two candidates are not told apart.
-// The fp32 score is off by less than 8 * 2^-24 (expf 2 ulp, a sum and a
-// division on values <= 1), the sum with the bias and the scaling to the key
-// by one unit each; two candidates and a margin give 16 units of 2^-24.
-constexpr unsigned kNear = 16;
+
+// What decides a token's order: the logits, or the scores (plus bias).
+enum RouteMode { kByLogit = 0, kBySigmoid = 1, kBySoftmax = 2 };
+
+// Candidates whose keys (23-bit values, see route_kernel) are this close are
+// not told apart by fp32.  In units of the key, for a pair:
+//   logits: m - x and the key each rounded once, 0.75 a candidate: under 2;
+//   sigmoid: the bias part of the key 1.5, the key's rounding 0.5, the score
+//     s (1 - s) (2^-22 + 1.5 |x| 2^-24) + s 2^-23 <= 1.7 a candidate: under 8;
+//   softmax: 2 + 2.5 (the exponential) a candidate, and the common factor 1 / sum
+//     (13 additions, their terms, a reciprocal: 20 * 2^-24) times at most 1: under 20.
+__host__ __device__ constexpr unsigned near_units(int mode) {
+  return mode == kByLogit ? 4u : mode == kBySigmoid ? 12u : 24u;
+}
 
 struct RouteParams {
   int64_t T;
@@ -35,6 +48,9 @@ struct RouteParams {
   int top_groups, group_top;
   int sigmoid, renorm;
   int by_logit;     // the logits' order decides (no bias, no sum of two scores)
+  int per_warp;     // consecutive tokens of one warp
+  int slots;        // of them, tokens whose weights are formed together
+  int seg;          // lanes per such token: k rounded up to a power of two
   float scale;
   const void* logits;
   const float* bias;
@@ -80,304 +96,511 @@ MOE_DEV void load_logits(const __nv_bfloat16* p, float* x) {
   }
 }
 
+// fp64 values as integers of the same order; 0 below all of them
+MOE_DEV unsigned long long ordered(double v) {
+  const long long b = __double_as_longlong(v);
+  return static_cast<unsigned long long>(b ^ ((b >> 63) | LLONG_MIN));
+}
+
 // The token's choices decided in fp64: lane j < k returns choice j's expert, or
-// -1.  buf: E doubles of this warp's shared memory.
-template <typename L>
-__device__ __noinline__ int route_exact(const RouteParams& p, int64_t t, double* buf) {
+// -1.  buf: E entries of this warp's shared memory.  Called for the few
+// tokens in a thousand that fp32 leaves open, by one warp while others are
+// done, so its chain of dependent steps counts: a choice is three integer
+// maxima (both halves of the value, then the lowest expert) and a search
+// through the winner's own candidates, and the loads and exponentials of a
+// lane's V candidates are independent.
+template <typename L, int V>
+__device__ int route_exact(const RouteParams& p, int64_t t, unsigned long long* buf) {
   const int lane = threadIdx.x & 31;
   const L* h = static_cast<const L*>(p.logits) + t * p.E;
-  double m = -INFINITY, sum = 0.0;
-  if (!p.by_logit && !p.sigmoid) {
+  // lane's candidates: experts first + lanes * i of its group
+  const int q = lane / p.lanes;
+  const int first = q * p.gs + (lane & (p.lanes - 1));
+  const int end = q < p.G ? (q + 1) * p.gs : 0;
+  float x[V], bias[V];
+#pragma unroll
+  for (int i = 0; i < V; ++i) {
+    const int e = first + p.lanes * i;
+    x[i] = e < end ? to_float(h[e]) : -INFINITY;
+    bias[i] = e < end && p.bias ? __ldg(p.bias + e) : 0.f;
+  }
+  double c[V];
+  if (p.by_logit) {
+#pragma unroll
+    for (int i = 0; i < V; ++i) c[i] = static_cast<double>(x[i]) + 0.0;  // -0 is +0
+  } else if (p.sigmoid) {
+#pragma unroll
+    for (int i = 0; i < V; ++i) c[i] = 1.0 / (1.0 + exp(-static_cast<double>(x[i])));
+  } else {
     float mf = -INFINITY;
-    for (int e = lane; e < p.E; e += 32) {
-      const float x = to_float(h[e]);
-      if (counts(x)) mf = fmaxf(mf, x);
-    }
-    m = warp_max(mf);
-    for (int e = lane; e < p.E; e += 32) {
-      const float x = to_float(h[e]);
-      if (counts(x)) sum += exp(static_cast<double>(x) - m);
+#pragma unroll
+    for (int i = 0; i < V; ++i) mf = counts(x[i]) ? fmaxf(mf, x[i]) : mf;
+    const double m = warp_max(mf);
+    double sum = 0.0;
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      c[i] = counts(x[i]) ? exp(static_cast<double>(x[i]) - m) : 0.0;
+      sum += c[i];
     }
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(kFull, sum, o);
+#pragma unroll
+    for (int i = 0; i < V; ++i) c[i] /= sum;
   }
-  for (int e = lane; e < p.E; e += 32) {
-    const float x = to_float(h[e]);
-    double c = -INFINITY;
-    if (counts(x)) {
-      const double xd = x;
-      if (p.by_logit) c = xd;
-      else c = p.sigmoid ? 1.0 / (1.0 + exp(-xd)) : exp(xd - m) / sum;
-      if (p.bias) {
-        const float b = __ldg(p.bias + e);
-        c = fabsf(b) < INFINITY ? c + static_cast<double>(b) : -INFINITY;
-      }
-    }
-    buf[e] = c;
+  double b1 = -INFINITY, b2 = -INFINITY;  // the lane's two best, then its group's
+#pragma unroll
+  for (int i = 0; i < V; ++i) {
+    const int e = first + p.lanes * i;
+    const bool can = counts(x[i]) && fabsf(bias[i]) < INFINITY;
+    c[i] = can ? c[i] + static_cast<double>(bias[i]) : -INFINITY;
+    if (e < end) buf[e] = can ? ordered(c[i]) : 0ull;
+    b2 = fmax(b2, fmin(b1, c[i]));
+    b1 = fmax(b1, c[i]);
   }
-  __syncwarp();
-  unsigned stay = kFull;
+  bool stays = true;
   if (p.G > 1) {
-    double v = -INFINITY;
-    if (lane < p.G) {  // a group per lane
-      double b1 = -INFINITY, b2 = -INFINITY;
-      for (int i = 0; i < p.gs; ++i) {
-        const double c = buf[lane * p.gs + i];
-        if (c > b1) { b2 = b1; b1 = c; }
-        else if (c > b2) b2 = c;
-      }
-      v = p.group_top == 2 && b2 > -INFINITY ? b1 + b2 : b1;
+    for (int o = 1; o < p.lanes; o <<= 1) {
+      const double o1 = __shfl_xor_sync(kFull, b1, o), o2 = __shfl_xor_sync(kFull, b2, o);
+      b2 = fmax(fmin(b1, o1), fmax(b2, o2));
+      b1 = fmax(b1, o1);
     }
+    const double v = p.group_top == 2 && b2 > -INFINITY ? b1 + b2 : b1;
     int rank = 0;
-    for (int q = 0; q < p.G; ++q) {
-      const double o = __shfl_sync(kFull, v, q);
-      rank += o > v || (o == v && q < lane);
+    for (int g = 0; g < p.G; ++g) {
+      const double o = __shfl_sync(kFull, v, g * p.lanes);
+      rank += o > v || (o == v && g < q);
     }
-    stay = __ballot_sync(kFull, lane < p.G && rank < p.top_groups);
+    stays = rank < p.top_groups;
   }
   int mine = -1;
+  unsigned long long best = 0ull;
+  int be = 0;
+  bool look = stays;  // the lane's best is not known yet
   for (int j = 0; j < p.k; ++j) {
-    double bv = -INFINITY;
-    int be = -1;
-    for (int e = lane; e < p.E; e += 32)
-      if (((stay >> (p.G > 1 ? e / p.gs : 0)) & 1u) && buf[e] > bv) { bv = buf[e]; be = e; }
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) {
-      const double ov = __shfl_xor_sync(kFull, bv, o);
-      const int oe = __shfl_xor_sync(kFull, be, o);
-      if (oe >= 0 && (be < 0 || ov > bv || (ov == bv && oe < be))) { bv = ov; be = oe; }
+    if (look) {
+      best = 0ull;
+      for (int e = first; e < end; e += p.lanes)
+        if (buf[e] > best) {
+          best = buf[e];
+          be = e;
+        }
+      look = false;
     }
-    if (be < 0) break;  // the same in every lane: nothing is left
-    if (lane == j) mine = be;
-    __syncwarp();
-    if (lane == 0) buf[be] = -INFINITY;
-    __syncwarp();
+    const unsigned hi = static_cast<unsigned>(best >> 32), lo = static_cast<unsigned>(best);
+    const unsigned top_hi = __reduce_max_sync(kFull, hi);
+    const unsigned top_lo = __reduce_max_sync(kFull, hi == top_hi ? lo : 0u);
+    if (top_hi == 0u && top_lo == 0u) break;  // the same in every lane: nothing is left
+    const bool among = hi == top_hi && lo == top_lo;
+    const int e = static_cast<int>(__reduce_min_sync(kFull, among ? static_cast<unsigned>(be) : ~0u));
+    if (lane == j) mine = e;
+    if (among && be == e) {
+      buf[e] = 0ull;
+      look = true;
+    }
   }
   __syncwarp();  // the buffer is free for the warp's next token
   return mine;
 }
 
-// Descending sort of N register values (N a power of two), a bitonic network.
+// sum and maximum over aligned segments of `seg` lanes (a power of two)
+MOE_DEV float seg_sum(float v, int seg) {
+  for (int o = seg >> 1; o > 0; o >>= 1) v += __shfl_xor_sync(kFull, v, o);
+  return v;
+}
+MOE_DEV float seg_max(float v, int seg) {
+  for (int o = seg >> 1; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(kFull, v, o));
+  return v;
+}
+
+// Weight of this lane's choice from its logit (-inf: none); the choices of a
+// token lie in one segment.  m, inv: the row's maximum and 1 / sum of
+// exponentials, for softmax weights that are not renormalised.
+MOE_DEV float choice_weight(const RouteParams& p, float x, float m, float inv) {
+  const bool there = x > -INFINITY;
+  if (!p.renorm) {
+    if (!there) return 0.f;
+    return p.scale * (p.sigmoid ? __fdividef(1.0f, 1.0f + expf(-x)) : expf(x - m) * inv);
+  }
+  // scaled by the largest choice so that small scores keep their ratio
+  const float mx = seg_max(x, p.seg);
+  const float ref = p.sigmoid ? fminf(mx, 0.f) : mx;
+  float w = 0.f;
+  if (there) {
+    const bool up = p.sigmoid && x >= 0.f;
+    w = expf(up ? -x : x - ref);
+    if (p.sigmoid) w = __fdividef(up ? 1.0f : w, 1.0f + (up ? w : expf(x)));
+  }
+  const float sum = seg_sum(w, p.seg);
+  return sum > 0.f ? p.scale * __fdividef(w, sum) : 0.f;
+}
+
+// A whole token through route_exact, by one warp.
+template <typename L, int V>
+__device__ __noinline__ void finish_exact(const RouteParams& p, int64_t t,
+                                          unsigned long long* buf) {
+  const int lane = threadIdx.x & 31;
+  const L* h = static_cast<const L*>(p.logits) + t * p.E;
+  const int e = route_exact<L, V>(p, t, buf);
+  float m = -INFINITY, inv = 0.f;
+  if (!p.sigmoid && !p.renorm) {
+    for (int i = lane; i < p.E; i += 32) {
+      const float x = to_float(h[i]);
+      if (counts(x)) m = fmaxf(m, x);
+    }
+    m = warp_max(m);
+    for (int i = lane; i < p.E; i += 32) {
+      const float x = to_float(h[i]);
+      if (counts(x)) inv += expf(x - m);
+    }
+    inv = warp_sum(inv);
+    inv = inv > 0.f ? 1.0f / inv : 0.f;
+  }
+  const float w = choice_weight(p, e >= 0 ? to_float(h[e]) : -INFINITY, m, inv);
+  if (lane < p.k) {
+    p.idx[t * p.k + lane] = e;
+    p.gate[t * p.k + lane] = w;
+  }
+}
+
+// Descending sort of N register values (N a power of two): Batcher's odd-even
+// merge network (1968), 19 exchanges for 8 values, 63 for 16.
 template <int N>
 MOE_DEV void sort_desc(uint32_t (&v)[N]) {
 #pragma unroll
-  for (int size = 2; size <= N; size <<= 1) {
+  for (int p = 1; p < N; p <<= 1) {
 #pragma unroll
-    for (int stride = size >> 1; stride > 0; stride >>= 1) {
+    for (int k = p; k >= 1; k >>= 1) {
 #pragma unroll
-      for (int i = 0; i < N; ++i) {
-        const int j = i ^ stride;
-        if (j > i) {
-          const bool down = (i & size) == 0;
-          const uint32_t hi = max(v[i], v[j]), lo = min(v[i], v[j]);
-          v[i] = down ? hi : lo;
-          v[j] = down ? lo : hi;
+      for (int lo = 0; lo < N; ++lo) {
+        const int hi = lo + k;
+        // pairs of the merge step: blocks of 2k from k % p on, inside one run of 2p
+        if (hi < N && lo >= k % p && (lo - k % p) % (2 * k) < k && lo / (2 * p) == hi / (2 * p)) {
+          const uint32_t a = max(v[lo], v[hi]);
+          v[hi] = min(v[lo], v[hi]);
+          v[lo] = a;
         }
       }
     }
   }
 }
 
+// A lane's sorted keys: the first in `head`, the others behind it in the lane's
+// column of shared memory (its own reads and writes only, so nothing waits).
+// Taking the first away is then one predicated load; shifting V registers costs V
+// instructions of the whole warp.
+template <int V>
+struct KeyList {
+  uint32_t head;
+  uint32_t next;  // shared-memory address
+  MOE_DEV void fill(const uint32_t (&key)[V], uint32_t column) {
+    head = key[0];
+#pragma unroll
+    for (int i = 1; i < V; ++i)
+      asm volatile("st.shared.u32 [%0], %1;" ::"r"(column + 128u * (i - 1)), "r"(key[i]) : "memory");
+    asm volatile("st.shared.u32 [%0], %1;" ::"r"(column + 128u * (V - 1)), "r"(0u) : "memory");
+    next = column;
+  }
+  // the first key, if it is `top` (the warp's largest; 0: nothing is left), goes
+  MOE_DEV void take(uint32_t top) {
+    if (head == top && top != 0u) {
+      asm volatile("ld.shared.u32 %0, [%1];" : "=r"(head) : "r"(next) : "memory");
+      next += 128u;
+    }
+  }
+};
+
+MOE_DEV float exp2_fast(float x) {  // 2 units in the last place; ftz
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+MOE_DEV float rcp_fast(float x) {  // 1 unit in the last place; ftz
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+constexpr float kLog2e = 1.4426950408889634f;
+
+MOE_DEV int expert_of(uint32_t key) { return 255 - static_cast<int>(key & 511u); }
+
+MOE_DEV float warp_max_redux(float v) {
+  float r;
+  asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(v));
+  return r;
+}
+
+// Blocks that fit an SM: 64 registers a thread up to 8 logits a lane, 80 above.
+__host__ __device__ constexpr int blocks_per_sm(int V) { return V <= 8 ? 4 : 3; }
+
+// Keys of one lane's V logits (their experts: e0 + (i / W) * lanes * W + i % W),
+// and for softmax weights the row's maximum and 1 / sum.  MASKED: some of
+// them, here or in another lane, may not count.
+template <typename L, int V, int W, int MODE, bool MASKED>
+MOE_DEV void make_keys(const RouteParams& p, const float (&x)[V], const float (&off)[V],
+                       float unit, int e0, bool sums, uint32_t (&key)[V], float& m, float& inv,
+                       bool& bad) {
+  constexpr bool kExactKey = MODE == kByLogit && sizeof(L) == 2;
+  bool can[V];
+#pragma unroll
+  for (int i = 0; i < V; ++i) {
+    can[i] = true;
+    if (MASKED) {
+      const bool fine = x[i] < INFINITY;  // false for NaN
+      bad |= !fine;
+      can[i] = fine && x[i] > kLowest;
+    }
+  }
+  if (sums || (MODE == kByLogit && !kExactKey)) {
+    m = -INFINITY;
+#pragma unroll
+    for (int i = 0; i < V; ++i) m = fmaxf(m, can[i] ? x[i] : -INFINITY);
+    m = warp_max_redux(m);
+  }
+  float s[V];
+  if (sums) {
+    float sum = 0.f;
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      s[i] = can[i] ? exp2_fast((x[i] - m) * kLog2e) : 0.f;
+      sum += s[i];
+    }
+    sum = warp_sum(sum);
+    inv = sum > 0.f ? __frcp_rn(sum) : 0.f;
+  }
+#pragma unroll
+  for (int i = 0; i < V; ++i) {
+    const uint32_t low = static_cast<uint32_t>(255 - e0 - (i / W) * p.lanes * W - i % W);
+    float v;
+    if constexpr (kExactKey) {  // the bits of a bf16 in ascending order, 1..65535
+      const uint32_t u = __float_as_uint(x[i] + 0.f) >> 16;  // -0 is +0
+      v = __uint_as_float((u & 0x8000u ? 0xffffu ^ u : u | 0x8000u) + 1u);
+    } else if constexpr (MODE == kByLogit) {
+      v = fmaxf(fmaf(m - x[i], -262144.0f, 16777214.0f), 8388609.0f);
+    } else {
+      const float sc = MODE == kBySigmoid ? rcp_fast(1.0f + exp2_fast(-kLog2e * x[i])) : s[i] * inv;
+      v = fmaf(sc, unit, off[i]);
+      if (MASKED) can[i] = can[i] && v > 0.f;  // not the NaN of a masked expert
+    }
+    key[i] = can[i] ? (__float_as_uint(v) << 9) + low : 0u;
+  }
+}
+
 // A warp per token.  Lane l holds V logits of one group (of the whole row
 // where there is no group limit).  Each candidate becomes a 32-bit key,
-// (rounded value in 24 bits) << 8 | (255 - expert): unique, larger is better,
-// ties in the value to the lower expert; 0 marks an expert that cannot be
-// chosen.  A lane sorts its keys once, and each choice is one warp-wide integer
-// maximum over the lanes' first keys.  The rounding to 24 bits is checked
-// afterwards: neighbours in the order (and the last choice against the first
-// one left out) that are within kNear units, and are not equal inputs, send
-// the token to route_exact.
-template <typename L, int V, int W>
-__global__ void __launch_bounds__(kWarps * 32) route_kernel(const __grid_constant__ RouteParams p) {
-  __shared__ double s_buf[kWarps][256];
+// (value in 23 bits) << 9 | (255 - expert): unique, larger is better, equal
+// values to the lower expert; 0 marks an expert that cannot be chosen.  The
+// value is the mantissa of a float between 2^23 and 2^24, so that a scale, an
+// offset and the rounding to an integer are one fused multiply-add.  A lane
+// sorts its keys once, and each choice is one warp-wide integer maximum over the
+// lanes' first keys.  The rounding is checked afterwards: where neighbours in
+// the order (or the last choice and one left out) are within near_units, and
+// are not equal inputs, the token is left open and the block's warps decide
+// the open ones in fp64 at the end (finish_exact), side by side.
+//
+// The scores here only decide, so they take the hardware's exp2 and reciprocal;
+// the weights of the k choices are formed from their logits with expf.  That
+// part uses k lanes, so a warp first collects the choices of `slots` tokens.
+// A token is a chain of dependent steps behind a load from memory, so the next
+// token's logits are on their way while one is decided.
+template <typename L, int V, int W, int MODE>
+__global__ void __launch_bounds__(kWarps * 32, blocks_per_sm(V))
+route_kernel(const __grid_constant__ RouteParams p) {
+  // per warp: the lanes' key lists, or route_exact's candidates
+  __shared__ union {
+    uint32_t column[V][32];
+    unsigned long long candidate[256];
+  } s_warp[kWarps];
+  __shared__ int32_t s_open[kMaxOpen];
+  __shared__ int s_num_open;
   dev::pdl_trigger();
+  if (threadIdx.x == 0) s_num_open = 0;
   dev::pdl_wait();
+  __syncthreads();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int q = lane / p.lanes, li = lane & (p.lanes - 1);
-  const int64_t nwarps = static_cast<int64_t>(gridDim.x) * kWarps;
-  const L* logits = static_cast<const L*>(p.logits);
-  constexpr bool kBf16 = sizeof(L) == 2;
-  const bool exact_key = kBf16 && p.by_logit;  // a bf16 logit fits the key
-  const bool has_bias = p.bias != nullptr;
+  constexpr bool kExactKey = MODE == kByLogit && sizeof(L) == 2;  // a bf16 logit fits the key
+  constexpr unsigned kNear = near_units(MODE);
+  const bool has_bias = MODE != kByLogit && p.bias != nullptr;
+  const bool sums = !p.sigmoid && (MODE == kBySoftmax || !p.renorm);  // weights need 1 / sum
   bool bad = false;
 
-  // this lane's experts: offset(i) = (i / W) * lanes * W + li * W + i % W within group q
+  // this lane's experts: first + (i / W) * lanes * W + li * W + i % W within group q
   const int first = q * p.gs;
-  float b[V];
-  float lo = 0.f, unit = 0.f;
-  if (!p.by_logit) {
+  float off[V];    // score modes: the bias's part of the key; NaN masks the expert
+  float unit = 0.f;
+  if constexpr (MODE != kByLogit) {
     float bmin = INFINITY, bmax = -INFINITY;
 #pragma unroll
     for (int i = 0; i < V; ++i) {
       const int o = (i / W) * p.lanes * W + li * W + i % W;
-      b[i] = 0.f;
+      off[i] = 0.f;
       if (q < p.G && o < p.gs) {
-        if (has_bias) b[i] = __ldg(p.bias + first + o);
-        if (!(fabsf(b[i]) < INFINITY)) {
-          if (!(b[i] < 0.f)) bad = true;  // NaN or +inf; -inf masks the expert
-          b[i] = -INFINITY;
+        if (has_bias) off[i] = __ldg(p.bias + first + o);
+        if (fabsf(off[i]) < INFINITY) {
+          bmin = fminf(bmin, off[i]);
+          bmax = fmaxf(bmax, off[i]);
         } else {
-          bmin = fminf(bmin, b[i]);
-          bmax = fmaxf(bmax, b[i]);
+          if (!(off[i] < 0.f)) bad = true;  // NaN or +inf; -inf masks the expert
+          off[i] = NAN;
         }
       }
     }
-    lo = -warp_max(-bmin);
-    unit = 16777213.0f / (1.0f + warp_max(bmax) - lo);
+    const float lo = -warp_max(-bmin);
+    unit = 8388600.0f / (1.0f + (warp_max(bmax) - lo));
+#pragma unroll
+    for (int i = 0; i < V; ++i)  // a range past fp32's: unit is 0 and fp64 decides
+      off[i] = off[i] == off[i] ? fminf(off[i] - lo, FLT_MAX) * unit + 8388610.0f : NAN;
   }
+  // every lane holds V logits of experts that its bias does not mask
+  bool whole = q < p.G && p.gs == p.lanes * V;
+  if constexpr (MODE != kByLogit) {
+#pragma unroll
+    for (int i = 0; i < V; ++i) whole = whole && off[i] == off[i];
+  }
+  whole = __all_sync(kFull, whole);
 
-  for (int64_t t = static_cast<int64_t>(blockIdx.x) * kWarps + warp; t < p.T; t += nwarps) {
-    const L* h = logits + t * p.E;
-    float x[V];
+  // the warp's tokens: tb .. tb + count - 1
+  const int64_t tb = (static_cast<int64_t>(blockIdx.x) * kWarps + warp) * p.per_warp;
+  const int count = tb < p.T ? static_cast<int>(min(static_cast<int64_t>(p.per_warp), p.T - tb)) : 0;
+  const L* rows = static_cast<const L*>(p.logits) + tb * p.E;
+  const L* from = rows + first + li * W;  // this lane's part of the next row to load
+  bool has[V / W];
+#pragma unroll
+  for (int c = 0; c < V / W; ++c) has[c] = q < p.G && li * W + c * p.lanes * W < p.gs;
+  auto load_row = [&](float (&x)[V]) {
 #pragma unroll
     for (int c = 0; c < V / W; ++c) {
-      const int o = c * p.lanes * W + li * W;
-      if (q < p.G && o < p.gs) {
-        load_logits<W>(h + first + o, x + c * W);
+      if (has[c]) {
+        load_logits<W>(from + c * p.lanes * W, x + c * W);
       } else {
 #pragma unroll
         for (int i = 0; i < W; ++i) x[c * W + i] = -INFINITY;
       }
     }
-    float m = -INFINITY;
-#pragma unroll
-    for (int i = 0; i < V; ++i) {
-      if (!counts(x[i])) {
-        if (!(x[i] < 0.f)) bad = true;  // NaN or +inf
-        x[i] = -INFINITY;
-      }
-      m = fmaxf(m, x[i]);
-    }
-    const bool softmax_sum = !p.sigmoid && (!p.by_logit || !p.renorm);
-    float inv = 0.f;
-    if (softmax_sum || (p.by_logit && !exact_key)) m = warp_max(m);
-    uint32_t key[V];
-    float s[V];
-    if (softmax_sum) {
-      float sum = 0.f;
-#pragma unroll
-      for (int i = 0; i < V; ++i) {
-        s[i] = x[i] > -INFINITY ? expf(x[i] - m) : 0.f;
-        sum += s[i];
-      }
-      sum = warp_sum(sum);
-      inv = sum > 0.f ? 1.0f / sum : 0.f;
-    }
-#pragma unroll
-    for (int i = 0; i < V; ++i) {
-      const int e = first + (i / W) * p.lanes * W + li * W + i % W;
-      uint32_t v;
-      bool can = x[i] > -INFINITY;
-      if (exact_key) {  // the bits of a bf16 in ascending order, 1..65535
-        const uint32_t u = __float_as_uint(x[i] + 0.f) >> 16;  // -0 is +0
-        v = (u & 0x8000u ? 0xffffu ^ u : u | 0x8000u) + 1u;
-      } else if (p.by_logit) {
-        v = 1u + static_cast<uint32_t>(fmaxf(16777213.0f - (m - x[i]) * 524288.0f, 0.f));
-      } else {
-        const float sc = p.sigmoid ? 1.0f / (1.0f + expf(-x[i])) : s[i] * inv;
-        can = can && b[i] > -INFINITY;
-        v = 1u + static_cast<uint32_t>(fminf(fmaxf((sc + b[i] - lo) * unit, 0.f), 16777213.0f));
-      }
-      key[i] = can ? (v << 8) | static_cast<uint32_t>(255 - e) : 0u;
-    }
-    sort_desc<V>(key);
+    from += p.E;
+  };
+  const uint32_t column = dev::smem_u32(&s_warp[warp].column[0][lane]);
+  // in the weights' part lane slot * seg + j works for choice j of a batch's token `slot`
+  const int my_slot = lane / p.seg, my_j = lane & (p.seg - 1);
 
-    bool unsure = false;
-    if (p.G > 1) {
-      uint32_t a1 = key[0], a2 = V > 1 ? key[V > 1 ? 1 : 0] : 0u;
-      for (int o = 1; o < p.lanes; o <<= 1) {
-        const uint32_t o1 = __shfl_xor_sync(kFull, a1, o), o2 = __shfl_xor_sync(kFull, a2, o);
-        a2 = max(min(a1, o1), max(a2, o2));
-        a1 = max(a1, o1);
-      }
-      uint32_t v = a1 >> 8;
-      if (p.group_top == 2) {
-        v += a2 >> 8;
-        unsure = __any_sync(kFull, a1 != 0u && a2 == 0u);  // a sum of one: its offset differs
-      }
-      uint32_t g = a1 ? (v << 5) | static_cast<uint32_t>(31 - q) : 0u;
-      bool stays = false;
-      uint32_t last = 0u;
-      for (int i = 0; i < p.top_groups; ++i) {
-        last = __reduce_max_sync(kFull, g);
-        if (g == last) {
-          stays = true;
-          g = 0u;
+  float ahead[V];
+  if (count > 0) load_row(ahead);
+  for (int done = 0; done < count; done += p.slots) {
+    const int in_batch = min(p.slots, count - done);
+    uint32_t mine = 0u;
+    float my_m = 0.f, my_inv = 0.f;
+    unsigned open = 0u;      // slots whose order fp32 could not tell
+    for (int slot = 0; slot < in_batch; ++slot) {
+      float x[V];
+#pragma unroll
+      for (int i = 0; i < V; ++i) x[i] = ahead[i];
+      if (done + slot + 1 < count) load_row(ahead);
+      // 0 unless a logit is masked, NaN or infinite (or above 1.7e38): the product
+      // overflows for the lowest values too, and inf * 0 is NaN
+      float odd = 0.f;
+#pragma unroll
+      for (int i = 0; i < V; ++i)
+        odd = fmaf(MODE == kBySigmoid ? -kLog2e * x[i] : x[i] + x[i], 0.f, odd);
+      uint32_t key[V];
+      float m = 0.f, inv = 0.f;
+      if (whole && __all_sync(kFull, odd == 0.f))
+        make_keys<L, V, W, MODE, false>(p, x, off, unit, first + li * W, sums, key, m, inv, bad);
+      else
+        make_keys<L, V, W, MODE, true>(p, x, off, unit, first + li * W, sums, key, m, inv, bad);
+      sort_desc<V>(key);
+
+      bool unsure = false;
+      if (p.G > 1) {
+        uint32_t a1 = key[0], a2 = V > 1 ? key[V > 1 ? 1 : 0] : 0u;
+        for (int o = 1; o < p.lanes; o <<= 1) {
+          const uint32_t o1 = __shfl_xor_sync(kFull, a1, o), o2 = __shfl_xor_sync(kFull, a2, o);
+          a2 = max(min(a1, o1), max(a2, o2));
+          a1 = max(a1, o1);
+        }
+        uint32_t v = a1 >> 9;
+        if (p.group_top == 2) {
+          v += a2 >> 9;
+          unsure = a1 != 0u && a2 == 0u;  // a sum of one: its offset differs
+        }
+        uint32_t g = a1 ? (v << 5) | static_cast<uint32_t>(31 - q) : 0u;  // 0: stays, or is empty
+        uint32_t last = 0u;
+#pragma unroll 4
+        for (int i = 0; i < p.top_groups; ++i) {
+          last = __reduce_max_sync(kFull, g);
+          if (g == last) g = 0u;
+        }
+        if (g != 0u) {
+          // a group left out that may be as good as the last one that stays
+          if (!kExactKey && (last >> 5) - (g >> 5) <= 2 * kNear) unsure = true;
+          key[0] = 0u;  // the list behind a 0 is never reached
         }
       }
-      const uint32_t next = __reduce_max_sync(kFull, g);
-      if (!exact_key && next != 0u && (last >> 5) - (next >> 5) <= 2 * kNear) unsure = true;
-      if (!stays) {
-#pragma unroll
-        for (int i = 0; i < V; ++i) key[i] = 0u;
+
+      KeyList<V> list;
+      list.fill(key, column);
+      uint32_t last = 0u;
+      const int rel = lane - slot * p.seg;
+#pragma unroll 4
+      for (int j = 0; j < p.k; ++j) {
+        last = __reduce_max_sync(kFull, list.head);
+        if (rel == j) mine = last;
+        list.take(last);
+      }
+      // the last choice against what this lane has left: close, and not the same inputs
+      if (!kExactKey && list.head != 0u && (last >> 9) - (list.head >> 9) <= kNear) {
+        const L* h = rows + static_cast<int64_t>(done + slot) * p.E;
+        const int el = expert_of(last);
+        const float xl = to_float(h[el]), bl = has_bias ? __ldg(p.bias + el) : 0.f;
+        while (list.head != 0u && (last >> 9) - (list.head >> 9) <= kNear) {
+          const int en = expert_of(list.head);
+          unsure |= to_float(h[en]) != xl || (has_bias && __ldg(p.bias + en) != bl);
+          list.take(list.head);
+        }
+      }
+      if (__any_sync(kFull, unsure)) open |= 1u << slot;
+      if (sums && my_slot == slot) {
+        my_m = m;
+        my_inv = inv;
       }
     }
 
-    uint32_t mine = 0u, last = 0u;
-    for (int j = 0; j < p.k; ++j) {
-      last = __reduce_max_sync(kFull, key[0]);
-      if (lane == j) mine = last;
-      if (key[0] == last) {
-#pragma unroll
-        for (int i = 0; i + 1 < V; ++i) key[i] = key[i + 1];
-        key[V - 1] = 0u;
-      }
-    }
-    int e = mine ? 255 - static_cast<int>(mine & 255u) : -1;
-    float xj = e >= 0 ? to_float(h[e]) : -INFINITY;
-    if (!exact_key && !unsure) {
+    const bool in = my_slot < in_batch && my_j < p.k;
+    const L* h = rows + static_cast<int64_t>(done) * p.E;
+    const int e = in && mine ? expert_of(mine) : -1;
+    const float xj = e >= 0 ? to_float(h[my_slot * p.E + e]) : -INFINITY;
+    if constexpr (!kExactKey) {
       const float bj = e >= 0 && has_bias ? __ldg(p.bias + e) : 0.f;
       const uint32_t after = __shfl_down_sync(kFull, mine, 1);
       const float xa = __shfl_down_sync(kFull, xj, 1), ba = __shfl_down_sync(kFull, bj, 1);
-      const bool close = lane + 1 < p.k && after != 0u && (mine >> 8) - (after >> 8) <= kNear &&
-                         !(xj == xa && bj == ba);
-      unsure = __any_sync(kFull, close);
-      if (last != 0u && !unsure) {
-        // the last choice against what was left out, past those equal to it
-        const float xl = __shfl_sync(kFull, xj, p.k - 1), bl = __shfl_sync(kFull, bj, p.k - 1);
-        for (;;) {
-          const uint32_t next = __reduce_max_sync(kFull, key[0]);
-          if (next == 0u || (last >> 8) - (next >> 8) > kNear) break;
-          const int en = 255 - static_cast<int>(next & 255u);
-          if (to_float(h[en]) != xl || (has_bias && __ldg(p.bias + en) != bl)) {
-            unsure = true;
-            break;
-          }
-          if (key[0] == next) {
-#pragma unroll
-            for (int i = 0; i + 1 < V; ++i) key[i] = key[i + 1];
-            key[V - 1] = 0u;
-          }
-        }
+      const bool close = in && my_j + 1 < p.k && after != 0u &&
+                         (mine >> 9) - (after >> 9) <= kNear && !(xj == xa && bj == ba);
+      for (unsigned c = __ballot_sync(kFull, close); c; c &= c - 1u)
+        open |= 1u << ((__ffs(c) - 1) / p.seg);
+    }
+    const float w = choice_weight(p, xj, my_m, my_inv);
+    if (in && !((open >> my_slot) & 1u)) {
+      const int64_t o = (tb + done) * p.k + my_slot * p.k + my_j;
+      p.idx[o] = e;
+      p.gate[o] = w;
+    }
+    for (; open; open &= open - 1u) {
+      const int64_t to = tb + done + __ffs(open) - 1;
+      if (lane == 0) {
+        const int n = atomicAdd(&s_num_open, 1);
+        if (n < kMaxOpen) s_open[n] = static_cast<int32_t>(to);
+        else p.idx[to * p.k] = kOpenMark;  // no room: found again below
       }
     }
-    if (unsure) {
-      e = route_exact<L>(p, t, s_buf[warp]);
-      xj = e >= 0 ? to_float(h[e]) : -INFINITY;
-    }
-
-    // weights: lane j holds choice j
-    float w;
-    if (p.renorm) {
-      // scaled by the largest choice so that small scores keep their ratio
-      const float mx = warp_max(xj);
-      const float ref = p.sigmoid ? fminf(mx, 0.f) : mx;
-      w = 0.f;
-      if (xj > -INFINITY) {
-        if (!p.sigmoid) w = expf(xj - ref);
-        else w = xj >= 0.f ? 1.0f / (1.0f + expf(-xj)) : expf(xj - ref) / (1.0f + expf(xj));
-      }
-      const float sum = warp_sum(w);
-      w = sum > 0.f ? p.scale * (w / sum) : 0.f;
-    } else {
-      w = 0.f;
-      if (xj > -INFINITY)
-        w = p.scale * (p.sigmoid ? 1.0f / (1.0f + expf(-xj)) : expf(xj - m) * inv);
-    }
-    if (lane < p.k) {
-      p.idx[t * p.k + lane] = e;
-      p.gate[t * p.k + lane] = w;
-    }
+  }
+  // (a call inside the loop above would keep its registers in local memory)
+  __syncthreads();
+  const int num_open = s_num_open;
+  for (int i = warp; i < min(num_open, kMaxOpen); i += kWarps)
+    finish_exact<L, V>(p, s_open[i], s_warp[warp].candidate);
+  if (num_open > kMaxOpen) {
+    for (int i = 0; i < count; ++i)
+      if (*static_cast<volatile int32_t*>(p.idx + (tb + i) * p.k) == kOpenMark)
+        finish_exact<L, V>(p, tb + i, s_warp[warp].candidate);
   }
   if (__any_sync(kFull, bad) && lane == 0 && p.status) atomicOr(p.status, MOE_STATUS_BAD_LOGIT);
 }
@@ -498,33 +721,44 @@ __global__ void __launch_bounds__(kWarps * 32) route_backward_kernel(const Route
   if (__any_sync(kFull, bad) && lane == 0 && p.status) atomicOr(p.status, MOE_STATUS_BAD_INDEX);
 }
 
-template <typename L, int V>
-void launch_route_v(const RouteParams& p, bool vec, unsigned grid, cudaStream_t s) {
-  if constexpr (V >= 4) {
-    if (vec) {
-      launch_pdl(route_kernel<L, V, 4>, dim3(grid), dim3(kWarps * 32), 0, s, p);
-      return;
-    }
-  }
-  launch_pdl(route_kernel<L, V, 1>, dim3(grid), dim3(kWarps * 32), 0, s, p);
-}
-
-template <typename L>
-void launch_route_t(const RouteParams& p, unsigned grid, cudaStream_t s) {
-  const bool vec = p.gs % 4 == 0;
-  const int per = vec ? (p.gs + 4 * p.lanes - 1) / (4 * p.lanes) * 4
-                      : (p.gs + p.lanes - 1) / p.lanes;
-  if (per <= 1) launch_route_v<L, 1>(p, false, grid, s);
-  else if (per <= 2) launch_route_v<L, 2>(p, false, grid, s);
-  else if (per <= 4) launch_route_v<L, 4>(p, vec, grid, s);
-  else if (per <= 8) launch_route_v<L, 8>(p, vec, grid, s);
-  else launch_route_v<L, 16>(p, vec, grid, s);
-}
-
 unsigned token_grid(int64_t T, int blocks_per_sm) {
   const int64_t want = (T + kWarps - 1) / kWarps;
   const int64_t most = static_cast<int64_t>(num_sms()) * blocks_per_sm;
   return static_cast<unsigned>(want < most ? want : most);
+}
+
+template <typename L, int V, int W>
+void launch_route_m(RouteParams p, cudaStream_t s) {
+  // a wave of blocks, each warp a run of consecutive tokens
+  const int64_t warps = static_cast<int64_t>(num_sms()) * blocks_per_sm(V) * kWarps;
+  p.per_warp = static_cast<int>((p.T + warps - 1) / warps);
+  p.slots = 32 / p.seg;
+  while (p.slots > p.per_warp) p.slots >>= 1;
+  const int64_t per_block = static_cast<int64_t>(p.per_warp) * kWarps;
+  const dim3 g(static_cast<unsigned>((p.T + per_block - 1) / per_block)), block(kWarps * 32);
+  if (p.by_logit) launch_pdl(route_kernel<L, V, W, kByLogit>, g, block, 0, s, p);
+  else if (p.sigmoid) launch_pdl(route_kernel<L, V, W, kBySigmoid>, g, block, 0, s, p);
+  else launch_pdl(route_kernel<L, V, W, kBySoftmax>, g, block, 0, s, p);
+}
+
+template <typename L, int V>
+void launch_route_v(const RouteParams& p, bool vec, cudaStream_t s) {
+  if constexpr (V >= 4) {
+    if (vec) return launch_route_m<L, V, 4>(p, s);
+  }
+  launch_route_m<L, V, 1>(p, s);
+}
+
+template <typename L>
+void launch_route_t(const RouteParams& p, cudaStream_t s) {
+  const bool vec = p.gs % 4 == 0;
+  const int per = vec ? (p.gs + 4 * p.lanes - 1) / (4 * p.lanes) * 4
+                      : (p.gs + p.lanes - 1) / p.lanes;
+  if (per <= 1) launch_route_v<L, 1>(p, false, s);
+  else if (per <= 2) launch_route_v<L, 2>(p, false, s);
+  else if (per <= 4) launch_route_v<L, 4>(p, vec, s);
+  else if (per <= 8) launch_route_v<L, 8>(p, vec, s);
+  else launch_route_v<L, 16>(p, vec, s);
 }
 
 }  // namespace
@@ -552,9 +786,10 @@ int32_t launch_route(const moe_route_config& c, const void* logits, const float*
   p.idx = expert_idx;
   p.gate = gate;
   p.status = status;
-  const unsigned grid = token_grid(c.T, 8);
-  if (c.dtype == MOE_DTYPE_BF16) launch_route_t<__nv_bfloat16>(p, grid, s);
-  else launch_route_t<float>(p, grid, s);
+  p.seg = 1;
+  while (p.seg < c.k) p.seg <<= 1;
+  if (c.dtype == MOE_DTYPE_BF16) launch_route_t<__nv_bfloat16>(p, s);
+  else launch_route_t<float>(p, s);
   return check_launch("route_kernel");
 }
 
