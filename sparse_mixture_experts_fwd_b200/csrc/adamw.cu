@@ -72,15 +72,40 @@ MOE_DEV float sqrt_fast(float x) {
   return r;
 }
 
-// p, m, v (fp32) -> their next values; returns sqrt(v)
-MOE_DEV float adam_one(float& p, float g, float& m, float& v, const AdamHyper& h,
-                       const StepScalars& s) {
+MOE_DEV float step_param(float p, float m, float r, const AdamHyper& h, const StepScalars& s) {
+  return fmaf(-s.rate, __fdividef(m, fmaf(r, s.root, h.eps)), p * s.decay);
+}
+
+// p, m, v (fp32) -> their next values
+MOE_DEV void adam_one(float& p, float g, float& m, float& v, const AdamHyper& h,
+                      const StepScalars& s) {
   g *= s.clip;
   m = fmaf(h.b1, m, h.nb1 * g);
   v = fmaf(h.b2, v, h.nb2 * g * g);
-  const float r = sqrt_fast(v);
-  p = fmaf(-s.rate, __fdividef(m, fmaf(r, s.root, h.eps)), p * s.decay);
-  return r;
+  p = step_param(p, m, sqrt_fast(v), h, s);
+}
+
+// The same where the moments are about to be rounded to 8 bits; v goes from
+// sqrt(v) to sqrt(v).  A code is a step of 6 to 12 percent, so one that falls
+// on the other side of a rounding border moves the next step visibly: every
+// product, sum and root here is rounded by itself, as the formula is written,
+// and the codes do not depend on how a compiler contracts it.
+MOE_DEV void adam_one8(float& p, float g, float& m, float& r, const AdamHyper& h,
+                       const StepScalars& s) {
+  g = __fmul_rn(g, s.clip);
+  m = __fadd_rn(__fmul_rn(h.b1, m), __fmul_rn(h.nb1, g));
+  const float v = __fadd_rn(__fmul_rn(h.b2, __fmul_rn(r, r)), __fmul_rn(__fmul_rn(h.nb2, g), g));
+  r = __fsqrt_rn(v);
+  p = step_param(p, m, r, h, s);
+}
+
+// a / b rounded to nearest from inv = 1 / b rounded to nearest (Markstein, "Computation
+// of elementary functions on the IBM RISC System/6000 processor", 1990): one
+// reciprocal serves a whole block.  Exact while a's residual is representable,
+// a > 1e-31; below that the codes may be off by one.
+MOE_DEV float quotient(float a, float b, float inv) {
+  const float q = a * inv;
+  return fmaf(fmaf(-q, b, a), inv, q);
 }
 
 MOE_DEV void load4(const float* p, float (&f)[4]) {
@@ -278,9 +303,8 @@ adamw8_kernel(const __grid_constant__ AdamBatch<N> b, const AdamHyper h) {
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
         fm[u][k] *= ms;
-        const float r = fr[u][k] * vs;
-        float sq = r * r;
-        fr[u][k] = adam_one(fp[u][k], fg[u][k], fm[u][k], sq, h, s);
+        fr[u][k] *= vs;
+        adam_one8(fp[u][k], fg[u][k], fm[u][k], fr[u][k], h, s);
         top_m = fmaxf(top_m, fabsf(fm[u][k]));
         top_r = fmaxf(top_r, fr[u][k]);
         // fmaxf drops a NaN: it has to reach the scale
@@ -293,8 +317,8 @@ adamw8_kernel(const __grid_constant__ AdamBatch<N> b, const AdamHyper h) {
     top_r = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(top_r)));
     const float sm = top_m >= kTiny ? top_m * (1.0f / 448.0f) : 0.f;
     const float sr = top_r * (1.0f / 448.0f);
-    const float im = sm > 0.f ? 448.0f / top_m : 0.f;
-    const float ir = sr > 0.f ? 448.0f / top_r : 0.f;
+    const float im = sm > 0.f ? __frcp_rn(sm) : 0.f;
+    const float ir = sr > 0.f ? __frcp_rn(sr) : 0.f;
     if (lane == 0) {
       t.ms[base / kQBlock] = sm;
       t.vs[base / kQBlock] = sr;
@@ -304,8 +328,8 @@ adamw8_kernel(const __grid_constant__ AdamBatch<N> b, const AdamHyper h) {
       const int64_t i = base + u * 128 + lane * 4;
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
-        fm[u][k] *= im;
-        const float x = fr[u][k] * ir;
+        fm[u][k] = quotient(fm[u][k], sm, im);
+        const float x = quotient(fr[u][k], sr, ir);
         fr[u][k] = fr[u][k] > 0.f ? fmaxf(x, 0.001953125f) : 0.f;  // 2^-9, the smallest code
       }
       qm[u] = to_e4m3x4(fm[u]);
