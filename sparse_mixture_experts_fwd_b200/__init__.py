@@ -164,8 +164,10 @@ def _ptr(t, name):
 
 
 def _stream(stream=None) -> int:
-    s = stream if stream is not None else torch.cuda.current_stream()
-    return s.cuda_stream
+    if stream is not None:
+        return stream.cuda_stream
+    # the handle alone: building torch's Stream object costs 3 us a call
+    return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
 
 
 def capacity(T: int, E: int, capacity_factor: float) -> int:
@@ -278,7 +280,7 @@ def _arg(t, name, dtype, shape):
     if t.shape != shape:
         raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
     p = _ptr(t, name)
-    if t.device.index != torch.cuda.current_device():
+    if t.get_device() != torch._C._cuda_getDevice():
         raise ValueError(f"{name} is on {t.device}, the current device is "
                          f"cuda:{torch.cuda.current_device()}")
     return p
@@ -354,6 +356,11 @@ def assign(cfg, expert_idx, out=None, status=None, stream=None):
     T, k, E, C = cfg.T, cfg.k, cfg.E, cfg.capacity
     ep = _arg(expert_idx, "expert_idx", torch.int32, (T, k))
     o = {} if out is None else out
+    if not o:  # one allocation for the int32 outputs: five of them cost 12 us
+        ints = _empty((T * k + E * C + 2 * E + 1,), torch.int32, expert_idx.device, stream)
+        slot, o["tok_of_row"], o["arrivals"], o["kept_cnt"], o["n_dropped"] = \
+            ints.split_with_sizes((T * k, E * C, E, E, 1))
+        o["slot"] = slot.view(T, k)
     ptrs = []
     for name, dtype, shape in (("slot", torch.int32, (T, k)), ("kept", torch.uint8, (T, k)),
                                ("tok_of_row", torch.int32, (E * C,)),
