@@ -15,6 +15,7 @@
 #include <algorithm>
 #include <cfloat>
 #include <cmath>
+#include <type_traits>
 #include <vector>
 
 #include "moe_internal.cuh"
@@ -24,7 +25,12 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kQBlock = 256;         // elements per scale: 8 per lane of one warp
-constexpr int kChunk = 2048;         // elements per block and round: 8 per thread
+constexpr int kRound = 2048;         // elements per block and round: 8 per thread
+// A chunk of a tensor is what a block (fp32 moments) or a warp (8-bit) takes at a
+// time: long where there are enough chunks for all of them, short where small
+// tensors would leave SMs idle.
+constexpr int kLongChunk = 4 * kRound;
+constexpr int kLongChunk8 = 8 * kQBlock, kShortChunk8 = kQBlock;
 constexpr int kMaxTensors = 4096;
 constexpr int kSmallBatch = 32;      // tensors in the small launch parameter block
 constexpr int kLargeBatch = 384;     // and in the large one (27 KB of the 32 KB limit)
@@ -58,6 +64,7 @@ struct AdamBatch {
   AdamTensor t[N];
   int32_t first[N + 1];             // first chunk of each tensor; first[n] = chunks in all
   int32_t n;
+  int32_t chunk;                    // elements per chunk
 };
 
 struct StepScalars {
@@ -72,8 +79,15 @@ MOE_DEV float sqrt_fast(float x) {
   return r;
 }
 
+MOE_DEV float rcp_fast(float x) {  // 1 unit in the last place; x >= eps, a normal number
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+
+// r: sqrt(v)
 MOE_DEV float step_param(float p, float m, float r, const AdamHyper& h, const StepScalars& s) {
-  return fmaf(-s.rate, __fdividef(m, fmaf(r, s.root, h.eps)), p * s.decay);
+  return fmaf(-s.rate, m * rcp_fast(fmaf(r, s.root, h.eps)), p * s.decay);
 }
 
 // p, m, v (fp32) -> their next values
@@ -85,18 +99,26 @@ MOE_DEV void adam_one(float& p, float g, float& m, float& v, const AdamHyper& h,
   p = step_param(p, m, sqrt_fast(v), h, s);
 }
 
-// The same where the moments are about to be rounded to 8 bits; v goes from
-// sqrt(v) to sqrt(v).  A code is a step of 6 to 12 percent, so one that falls
-// on the other side of a rounding border moves the next step visibly: every
-// product, sum and root here is rounded by itself, as the formula is written,
-// and the codes do not depend on how a compiler contracts it.
-MOE_DEV void adam_one8(float& p, float g, float& m, float& r, const AdamHyper& h,
-                       const StepScalars& s) {
+// The moments that are about to be rounded to 8 bits; v goes from sqrt(v) to v.
+// A code is a step of 6 to 12 percent, so one that falls on the other side of a
+// rounding border moves the next step visibly: every product and sum here is
+// rounded by itself, as the formula is written, and the codes do not depend on
+// how a compiler contracts it.
+MOE_DEV void moments8(float g, float& m, float& v, const AdamHyper& h, const StepScalars& s) {
   g = __fmul_rn(g, s.clip);
   m = __fadd_rn(__fmul_rn(h.b1, m), __fmul_rn(h.nb1, g));
-  const float v = __fadd_rn(__fmul_rn(h.b2, __fmul_rn(r, r)), __fmul_rn(__fmul_rn(h.nb2, g), g));
-  r = __fsqrt_rn(v);
-  p = step_param(p, m, r, h, s);
+  v = __fadd_rn(__fmul_rn(h.b2, __fmul_rn(v, v)), __fmul_rn(__fmul_rn(h.nb2, g), g));
+}
+
+// sqrt(v) for v >= kSmallV: one Heron step, r - (r^2 - v) / (2 r), on the hardware's
+// approximation, its residual exact in the fused product.  The step's own error is
+// below 2^-42, so the result is the rounded root but for one value in 2^18.
+constexpr float kSmallV = 1e-36f;
+MOE_DEV float root_heron(float v) {
+  float y;
+  asm("rsqrt.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(v));
+  const float r = v * y;
+  return fmaf(fmaf(-r, r, v), 0.5f * y, r);
 }
 
 // a / b rounded to nearest from inv = 1 / b rounded to nearest (Markstein, "Computation
@@ -188,10 +210,10 @@ MOE_DEV int tensor_of(const AdamBatch<N>& b, int c) {
   return lo;
 }
 
-// A round handles kChunk elements: thread i takes the 4 at 4 i and the 4 at
-// 1024 + 4 i, so that every load of a warp is one contiguous run.
+// In a round thread i takes the 4 elements at 4 i and the 4 at 1024 + 4 i, so that
+// every load of a warp is one contiguous run.
 template <typename G, int N>
-__global__ void __launch_bounds__(kThreads)
+__global__ void __launch_bounds__(kThreads, 5)
 adamw_kernel(const __grid_constant__ AdamBatch<N> b, const AdamHyper h) {
   __shared__ StepScalars s_step;
   dev::pdl_trigger();
@@ -206,13 +228,15 @@ adamw_kernel(const __grid_constant__ AdamBatch<N> b, const AdamHyper h) {
   for (int c = blockIdx.x; c < b.first[b.n]; c += gridDim.x) {
     const int n = tensor_of(b, c);
     const AdamTensor& t = b.t[n];
-    const int64_t base = static_cast<int64_t>(c - b.first[n]) * kChunk;
+    const int64_t chunk = static_cast<int64_t>(c - b.first[n]) * b.chunk;
+    const int64_t end = min(chunk + b.chunk, t.len);
     float* p = t.p;
     const G* g = static_cast<const G*>(t.g);
     float* m = static_cast<float*>(t.m);
     float* v = static_cast<float*>(t.v);
-    float fp[2][4], fg[2][4], fm[2][4], fv[2][4];
-    if (base + kChunk <= t.len) {
+    int64_t base = chunk;
+    for (; base + kRound <= end; base += kRound) {
+      float fp[2][4], fg[2][4], fm[2][4], fv[2][4];
 #pragma unroll
       for (int u = 0; u < 2; ++u) {
         const int64_t i = base + u * (kThreads * 4) + threadIdx.x * 4;
@@ -231,24 +255,160 @@ adamw_kernel(const __grid_constant__ AdamBatch<N> b, const AdamHyper h) {
         store4(v + i, fv[u]);
         if (t.copy) store4(t.copy + i, fp[u]);
       }
-    } else {
-      for (int64_t i = base + threadIdx.x; i < t.len; i += kThreads) {
-        float x = p[i], y = m[i], z = v[i];
-        adam_one(x, load1(g + i), y, z, h, s);
-        p[i] = x;
-        m[i] = y;
-        v[i] = z;
-        if (t.copy) t.copy[i] = __float2bfloat16_rn(x);
-      }
+    }
+    for (int64_t i = base + threadIdx.x; i < end; i += kThreads) {
+      float x = p[i], y = m[i], z = v[i];
+      adam_one(x, load1(g + i), y, z, h, s);
+      p[i] = x;
+      m[i] = y;
+      v[i] = z;
+      if (t.copy) t.copy[i] = __float2bfloat16_rn(x);
     }
   }
 }
 
 // 8-bit moments: a warp owns the 256 elements of one scale, 4 at 4 l and 4 at
 // 128 + 4 l per lane l.
+template <typename G>
+struct Block8 {
+  float p[2][4], g[2][4];
+  uint32_t qm[2], qv[2];
+  float ms, vs;
+
+  // p, the codes and the scales of the next step
+  MOE_DEV void step(const AdamHyper& h, const StepScalars& s) {
+    float m[2][4], r[2][4];
+    float least = INFINITY;
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+      of_e4m3x4(qm[u], m[u]);
+      of_e4m3x4(qv[u], r[u]);
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        m[u][k] *= ms;
+        r[u][k] *= vs;
+        moments8(g[u][k], m[u][k], r[u][k], h, s);
+        least = fminf(least, r[u][k]);
+      }
+    }
+    const bool usual = least >= kSmallV;  // else zeros, or what the approximation would flush
+    if (usual) {
+#pragma unroll
+      for (int u = 0; u < 2; ++u)
+#pragma unroll
+        for (int k = 0; k < 4; ++k) r[u][k] = root_heron(r[u][k]);
+    } else {
+#pragma unroll
+      for (int u = 0; u < 2; ++u)
+#pragma unroll
+        for (int k = 0; k < 4; ++k) r[u][k] = sqrtf(r[u][k]);
+    }
+    // magnitudes keep their order as integers, and a NaN is above all of them
+    uint32_t bits_m = 0u, bits_r = 0u;
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        p[u][k] = step_param(p[u][k], m[u][k], r[u][k], h, s);
+        bits_m = max(bits_m, __float_as_uint(fabsf(m[u][k])));
+        bits_r = max(bits_r, __float_as_uint(r[u][k]));
+      }
+    }
+    const float top_m = __uint_as_float(__reduce_max_sync(0xffffffffu, bits_m));
+    const float top_r = __uint_as_float(__reduce_max_sync(0xffffffffu, bits_r) & 0x7fffffffu);
+    // (a NaN fails the comparison: it becomes the scale)
+    ms = top_m < kTiny ? 0.f : top_m * (1.0f / 448.0f);
+    vs = top_r * (1.0f / 448.0f);
+    const float im = ms == 0.f ? 0.f : __frcp_rn(ms);
+    const float ir = vs == 0.f ? 0.f : __frcp_rn(vs);
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        m[u][k] = quotient(m[u][k], ms, im);
+        // 2^-9, the smallest code, unless v is 0
+        r[u][k] = fmaxf(quotient(r[u][k], vs, ir), usual || r[u][k] > 0.f ? 0.001953125f : 0.f);
+      }
+      qm[u] = to_e4m3x4(m[u]);
+      qv[u] = to_e4m3x4(r[u]);
+    }
+  }
+
+  // a block behind whose 256 elements the tensor ends: one element at a time
+  MOE_DEV void load_tail(const AdamTensor& t, int64_t base, int lane) {
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+      qm[u] = qv[u] = 0u;
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const int64_t i = base + u * 128 + lane * 4 + k;
+        p[u][k] = g[u][k] = 0.f;
+        if (i < t.len) {
+          p[u][k] = t.p[i];
+          g[u][k] = load1(static_cast<const G*>(t.g) + i);
+          qm[u] |= static_cast<uint32_t>(static_cast<const uint8_t*>(t.m)[i]) << (8 * k);
+          qv[u] |= static_cast<uint32_t>(static_cast<const uint8_t*>(t.v)[i]) << (8 * k);
+        }
+      }
+    }
+  }
+
+  MOE_DEV void store(const AdamTensor& t, int64_t base, int lane) const {
+    uint8_t* m_ = static_cast<uint8_t*>(t.m);
+    uint8_t* v_ = static_cast<uint8_t*>(t.v);
+    const bool full = base + kQBlock <= t.len;
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+      const int64_t i = base + u * 128 + lane * 4;
+      if (full) {
+        store4(t.p + i, p[u]);
+        *reinterpret_cast<uint32_t*>(m_ + i) = qm[u];
+        *reinterpret_cast<uint32_t*>(v_ + i) = qv[u];
+        if (t.copy) store4(t.copy + i, p[u]);
+      } else {
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          if (i + k < t.len) {
+            t.p[i + k] = p[u][k];
+            m_[i + k] = static_cast<uint8_t>(qm[u] >> (8 * k));
+            v_[i + k] = static_cast<uint8_t>(qv[u] >> (8 * k));
+            if (t.copy) t.copy[i + k] = __float2bfloat16_rn(p[u][k]);
+          }
+        }
+      }
+    }
+  }
+};
+
+template <int BYTES>
+MOE_DEV void copy_async(void* smem, const void* global) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(dev::smem_u32(smem)), "l"(global),
+               "n"(BYTES)
+               : "memory");
+}
+MOE_DEV void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int PENDING>
+MOE_DEV void copy_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(PENDING) : "memory"); }
+
+// The arithmetic on a block takes as long as its loads, and loads held in registers
+// would leave too few warps to overlap them.  So a thread copies its part of the
+// next block into its own places in shared memory (asynchronous copies, waited
+// for by the thread that issued them: no barrier) while it works on one.
+template <typename G>
+struct Stage8 {
+  float4 p[2][kThreads];
+  typename std::conditional<sizeof(G) == 4, float4, uint2>::type g[2][kThreads];
+  uint32_t m[2][kThreads], v[2][kThreads];
+};
+
+// A warp takes a chunk of up to 8 consecutive blocks: their scales are one
+// 32-byte sector, loaded and stored at once by 8 lanes.  (One 4-byte store per
+// block costs 100 of 520 us on 184 M parameters: partial sectors.)
 template <typename G, int N>
-__global__ void __launch_bounds__(kThreads)
+__global__ void __launch_bounds__(kThreads, 3)
 adamw8_kernel(const __grid_constant__ AdamBatch<N> b, const AdamHyper h) {
+  extern __shared__ __align__(16) uint8_t s_mem[];
+  Stage8<G>* stage = reinterpret_cast<Stage8<G>*>(s_mem);  // [2]
   __shared__ StepScalars s_step;
   dev::pdl_trigger();
   dev::pdl_wait();
@@ -259,99 +419,93 @@ adamw8_kernel(const __grid_constant__ AdamBatch<N> b, const AdamHyper h) {
     if (blockIdx.x == 0 && threadIdx.x == 0 && h.status) atomicOr(h.status, MOE_STATUS_NONFINITE);
     return;
   }
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  for (int c = blockIdx.x; c < b.first[b.n]; c += gridDim.x) {
-    const int n = tensor_of(b, c);
-    const AdamTensor& t = b.t[n];
-    const int64_t base = static_cast<int64_t>(c - b.first[n]) * kChunk + warp * kQBlock;
-    if (base >= t.len) continue;  // the same for the whole warp
-    float* p = t.p;
-    const G* g = static_cast<const G*>(t.g);
-    uint8_t* m = static_cast<uint8_t*>(t.m);
-    uint8_t* v = static_cast<uint8_t*>(t.v);
-    const bool full = base + kQBlock <= t.len;
-    float fp[2][4], fg[2][4], fm[2][4], fr[2][4];
-    uint32_t qm[2], qv[2];
-    const float ms = t.ms[base / kQBlock], vs = t.vs[base / kQBlock];
+  const int tid = threadIdx.x, lane = tid & 31;
+  const int stride = gridDim.x * (kThreads / 32);
+  const int chunks = b.first[b.n];
+  const int run = b.chunk / kQBlock;  // 8 or 1
+
+  // a place in the warp's sequence of blocks
+  struct Place {
+    int c, n, i;        // chunk, its tensor, block in the chunk
+    int64_t start, end;  // elements of the chunk in the tensor
+  };
+  auto enter = [&](Place& q) {  // chunk q.c; the tensors are met in order
+    if (q.c >= chunks) return;
+    while (b.first[q.n + 1] <= q.c) ++q.n;
+    q.i = 0;
+    q.start = static_cast<int64_t>(q.c - b.first[q.n]) * b.chunk;
+    q.end = min(q.start + b.chunk, b.t[q.n].len);
+  };
+  auto advance = [&](Place& q) {
+    if (q.start + (++q.i) * kQBlock < q.end) return;
+    q.c += stride;
+    enter(q);
+  };
+  Place ahead{static_cast<int>(blockIdx.x) * (kThreads / 32) + (tid >> 5), 0, 0, 0, 0};
+  enter(ahead);
+  Place now = ahead;
+  float ms_ahead = 0.f, vs_ahead = 0.f;  // lane i: scale of the chunk's block i
+  auto fetch = [&](Stage8<G>& st) {
+    if (ahead.c < chunks) {
+      const AdamTensor& t = b.t[ahead.n];
+      if (ahead.i == 0 && lane < run && ahead.start + lane * kQBlock < ahead.end) {
+        ms_ahead = t.ms[ahead.start / kQBlock + lane];
+        vs_ahead = t.vs[ahead.start / kQBlock + lane];
+      }
+      const int64_t base = ahead.start + ahead.i * kQBlock;
+      if (base + kQBlock <= t.len) {
+        const int64_t i = base + lane * 4;
 #pragma unroll
-    for (int u = 0; u < 2; ++u) {
-      const int64_t i = base + u * 128 + lane * 4;
-      if (full) {
-        load4(p + i, fp[u]);
-        load4(g + i, fg[u]);
-        qm[u] = *reinterpret_cast<const uint32_t*>(m + i);
-        qv[u] = *reinterpret_cast<const uint32_t*>(v + i);
-      } else {
-        qm[u] = qv[u] = 0u;
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          const bool in = i + k < t.len;
-          fp[u][k] = in ? p[i + k] : 0.f;
-          fg[u][k] = in ? load1(g + i + k) : 0.f;
-          if (in) {
-            qm[u] |= static_cast<uint32_t>(m[i + k]) << (8 * k);
-            qv[u] |= static_cast<uint32_t>(v[i + k]) << (8 * k);
-          }
+        for (int u = 0; u < 2; ++u) {
+          copy_async<16>(&st.p[u][tid], t.p + i + u * 128);
+          copy_async<sizeof(st.g[u][tid])>(&st.g[u][tid], static_cast<const G*>(t.g) + i + u * 128);
+          copy_async<4>(&st.m[u][tid], static_cast<const uint8_t*>(t.m) + i + u * 128);
+          copy_async<4>(&st.v[u][tid], static_cast<const uint8_t*>(t.v) + i + u * 128);
         }
       }
+      advance(ahead);
     }
-    float top_m = 0.f, top_r = 0.f;
+    copy_commit();
+  };
+  fetch(stage[0]);
+  float ms = 0.f, vs = 0.f;
+  for (int slot = 0; now.c < chunks; slot ^= 1) {
+    if (now.i == 0) {
+      ms = ms_ahead;
+      vs = vs_ahead;
+    }
+    fetch(stage[slot ^ 1]);
+    copy_wait<1>();
+    const AdamTensor& t = b.t[now.n];
+    const int64_t base = now.start + now.i * kQBlock;
+    Block8<G> x;
+    if (base + kQBlock <= t.len) {
+      const Stage8<G>& st = stage[slot];
 #pragma unroll
-    for (int u = 0; u < 2; ++u) {
-      of_e4m3x4(qm[u], fm[u]);
-      of_e4m3x4(qv[u], fr[u]);
-#pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        fm[u][k] *= ms;
-        fr[u][k] *= vs;
-        adam_one8(fp[u][k], fg[u][k], fm[u][k], fr[u][k], h, s);
-        top_m = fmaxf(top_m, fabsf(fm[u][k]));
-        top_r = fmaxf(top_r, fr[u][k]);
-        // fmaxf drops a NaN: it has to reach the scale
-        if (!(fabsf(fm[u][k]) < INFINITY)) top_m = INFINITY;
-        if (!(fr[u][k] < INFINITY)) top_r = INFINITY;
+      for (int u = 0; u < 2; ++u) {
+        load4(reinterpret_cast<const float*>(&st.p[u][tid]), x.p[u]);
+        load4(reinterpret_cast<const G*>(&st.g[u][tid]), x.g[u]);
+        x.qm[u] = st.m[u][tid];
+        x.qv[u] = st.v[u][tid];
       }
+    } else {
+      x.load_tail(t, base, lane);
     }
-    // non-negative floats keep their order as integers
-    top_m = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(top_m)));
-    top_r = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(top_r)));
-    const float sm = top_m >= kTiny ? top_m * (1.0f / 448.0f) : 0.f;
-    const float sr = top_r * (1.0f / 448.0f);
-    const float im = sm > 0.f ? __frcp_rn(sm) : 0.f;
-    const float ir = sr > 0.f ? __frcp_rn(sr) : 0.f;
-    if (lane == 0) {
-      t.ms[base / kQBlock] = sm;
-      t.vs[base / kQBlock] = sr;
+    x.ms = __shfl_sync(0xffffffffu, ms, now.i);
+    x.vs = __shfl_sync(0xffffffffu, vs, now.i);
+    x.step(h, s);
+    x.store(t, base, lane);
+    if (lane == now.i) {
+      ms = x.ms;
+      vs = x.vs;
     }
-#pragma unroll
-    for (int u = 0; u < 2; ++u) {
-      const int64_t i = base + u * 128 + lane * 4;
-#pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        fm[u][k] = quotient(fm[u][k], sm, im);
-        const float x = quotient(fr[u][k], sr, ir);
-        fr[u][k] = fr[u][k] > 0.f ? fmaxf(x, 0.001953125f) : 0.f;  // 2^-9, the smallest code
-      }
-      qm[u] = to_e4m3x4(fm[u]);
-      qv[u] = to_e4m3x4(fr[u]);
-      if (full) {
-        store4(p + i, fp[u]);
-        *reinterpret_cast<uint32_t*>(m + i) = qm[u];
-        *reinterpret_cast<uint32_t*>(v + i) = qv[u];
-        if (t.copy) store4(t.copy + i, fp[u]);
-      } else {
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          if (i + k < t.len) {
-            p[i + k] = fp[u][k];
-            m[i + k] = static_cast<uint8_t>(qm[u] >> (8 * k));
-            v[i + k] = static_cast<uint8_t>(qv[u] >> (8 * k));
-            if (t.copy) t.copy[i + k] = __float2bfloat16_rn(fp[u][k]);
-          }
-        }
-      }
+    if (base + kQBlock >= now.end && lane <= now.i) {
+      t.ms[now.start / kQBlock + lane] = ms;
+      t.vs[now.start / kQBlock + lane] = vs;
     }
+    advance(now);
   }
+  copy_wait<0>();
 }
 
 struct Lists {
@@ -397,8 +551,8 @@ int32_t check_lists(const moe_adamw_config* c, int32_t n, const Lists& l) {
     }
     if (l.copy && l.copy[i] && !aligned16(l.copy[i]))
       return fail(MOE_ERR_ALIGNMENT, "moe_adamw: bf16 copy not 16-byte aligned");
-    chunks += (l.len[i] + kChunk - 1) / kChunk;
-    if (chunks > 2147483647) return fail(MOE_ERR_UNSUPPORTED, "moe_adamw: more than 2^42 elements");
+    chunks += (l.len[i] + kRound - 1) / kRound;  // (the short 8-bit chunk is not used for that many)
+    if (chunks > (1 << 30)) return fail(MOE_ERR_UNSUPPORTED, "moe_adamw: more than 2^41 elements");
   }
   return MOE_OK;
 }
@@ -422,10 +576,16 @@ int32_t check_hyper(const moe_adamw_config* c, const double* norm, const double*
 template <typename G, int N>
 void launch_batch(const AdamBatch<N>& b, const AdamHyper& h, bool bits8, cudaStream_t s) {
   const int chunks = b.first[b.n];
-  const int most = num_sms() * 8;
-  const dim3 grid(static_cast<unsigned>(std::min(chunks, most)));
-  if (bits8) launch_pdl(adamw8_kernel<G, N>, grid, dim3(kThreads), 0, s, b, h);
-  else launch_pdl(adamw_kernel<G, N>, grid, dim3(kThreads), 0, s, b, h);
+  if (bits8) {
+    constexpr size_t kSmem = 2 * sizeof(Stage8<G>);
+    const int blocks = (chunks + kThreads / 32 - 1) / (kThreads / 32);
+    const dim3 grid(static_cast<unsigned>(std::min(blocks, num_sms() * 3)));
+    cudaFuncSetAttribute(adamw8_kernel<G, N>, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(kSmem));
+    launch_pdl(adamw8_kernel<G, N>, grid, dim3(kThreads), kSmem, s, b, h);
+    return;
+  }
+  const dim3 grid(static_cast<unsigned>(std::min(chunks, num_sms() * 8)));
+  launch_pdl(adamw_kernel<G, N>, grid, dim3(kThreads), 0, s, b, h);
 }
 
 template <int N>
@@ -433,6 +593,10 @@ int32_t run_batches(const moe_adamw_config& c, int32_t n, const Lists& l, const 
                     cudaStream_t s) {
   AdamBatch<N> b;
   const bool bits8 = c.state_bits == 8;
+  int64_t all = 0;
+  for (int32_t i = 0; i < n; ++i) all += l.len[i];
+  if (bits8) b.chunk = all >= static_cast<int64_t>(num_sms()) * 64 * kLongChunk8 ? kLongChunk8 : kShortChunk8;
+  else b.chunk = all >= static_cast<int64_t>(num_sms()) * 32 * kLongChunk ? kLongChunk : kRound;
   for (int32_t i = 0; i < n;) {
     b.n = 0;
     b.first[0] = 0;
@@ -441,7 +605,7 @@ int32_t run_batches(const moe_adamw_config& c, int32_t n, const Lists& l, const 
       b.t[b.n] = AdamTensor{l.param[i], l.grad[i], l.m[i], l.v[i], bits8 ? l.ms[i] : nullptr,
                             bits8 ? l.vs[i] : nullptr,
                             l.copy ? static_cast<__nv_bfloat16*>(l.copy[i]) : nullptr, l.len[i]};
-      b.first[b.n + 1] = b.first[b.n] + static_cast<int32_t>((l.len[i] + kChunk - 1) / kChunk);
+      b.first[b.n + 1] = b.first[b.n] + static_cast<int32_t>((l.len[i] + b.chunk - 1) / b.chunk);
       ++b.n;
     }
     if (b.n == 0) break;

@@ -146,6 +146,33 @@ def test_tensor_counts(moe, bits, n):
 
 
 @pytest.mark.parametrize("bits", [32, 8])
+def test_long_tensors_equal_their_pieces(moe, bits):
+    """One call on 45 M elements (long chunks) gives the bits of calls on its pieces (short ones)."""
+    n, cuts = 45_000_123, [0, 15_000_064, 30_000_128, 45_000_123]   # cuts at blocks of 256
+    dev = "cuda"
+    gen = torch.Generator(device=dev).manual_seed(3)
+    p = 0.02 * torch.randn(n, generator=gen, device=dev)
+    g = (1e-3 * torch.randn(n, generator=gen, device=dev)).bfloat16()
+    state = moe.adamw_state([p], bits)
+    whole = moe.adamw_tensors([p], [g], **state)
+    q, other = p.clone(), {}
+    other = moe.adamw_state([q], bits)
+    parts = []
+    for a, b in zip(cuts, cuts[1:]):
+        cut = {k: [v[0][a // 256:-(-b // 256)] if k.endswith("scale") else v[0][a:b]]
+               for k, v in other.items()}
+        parts.append(moe.adamw_tensors([q[a:b]], [g[a:b]], **cut))
+    for step in (1, 2):
+        moe.adamw_step(whole, step=step, **HYPER)
+        for ts in parts:
+            moe.adamw_step(ts, step=step, **HYPER)
+        assert torch.equal(p, q)
+        for k in state:
+            assert torch.equal(state[k][0].view(torch.uint8), other[k][0].view(torch.uint8)), k
+    assert not torch.equal(p[:1000], torch.zeros(1000, device=dev))
+
+
+@pytest.mark.parametrize("bits", [32, 8])
 def test_clip_by_the_sparseclip_norm(moe, bits):
     before = make([5000, 777, 2048], bits, torch.float32, seed=5)
     D, ts, raws = on_device(moe, before, bits)
