@@ -356,11 +356,19 @@ def assign(cfg, expert_idx, out=None, status=None, stream=None):
     T, k, E, C = cfg.T, cfg.k, cfg.E, cfg.capacity
     ep = _arg(expert_idx, "expert_idx", torch.int32, (T, k))
     o = {} if out is None else out
-    if not o:  # one allocation for the int32 outputs: five of them cost 12 us
-        ints = _empty((T * k + E * C + 2 * E + 1,), torch.int32, expert_idx.device, stream)
+    if not o:  # one allocation for the int32 outputs (five cost 12 us), pointers by offset
+        n = T * k
+        ints = _empty((n + E * C + 2 * E + 1,), torch.int32, expert_idx.device, stream)
         slot, o["tok_of_row"], o["arrivals"], o["kept_cnt"], o["n_dropped"] = \
-            ints.split_with_sizes((T * k, E * C, E, E, 1))
+            ints.split_with_sizes((n, E * C, E, E, 1))
         o["slot"] = slot.view(T, k)
+        o["kept"] = _empty((T, k), torch.uint8, expert_idx.device, stream)
+        at = ints.data_ptr()
+        _check(lib.moe_assign(ctypes.byref(cfg), ep, at, o["kept"].data_ptr(), at + 4 * n,
+                              at + 4 * (n + E * C), at + 4 * (n + E * C + E),
+                              at + 4 * (n + E * C + 2 * E), _status(status), _stream(stream)),
+               "moe_assign")
+        return o
     ptrs = []
     for name, dtype, shape in (("slot", torch.int32, (T, k)), ("kept", torch.uint8, (T, k)),
                                ("tok_of_row", torch.int32, (E * C,)),

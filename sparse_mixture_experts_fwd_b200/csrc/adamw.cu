@@ -85,49 +85,85 @@ MOE_DEV float rcp_fast(float x) {  // 1 unit in the last place; x >= eps, a norm
   return r;
 }
 
-// r: sqrt(v)
-MOE_DEV float step_param(float p, float m, float r, const AdamHyper& h, const StepScalars& s) {
-  return fmaf(-s.rate, m * rcp_fast(fmaf(r, s.root, h.eps)), p * s.decay);
-}
-
 // p, m, v (fp32) -> their next values
 MOE_DEV void adam_one(float& p, float g, float& m, float& v, const AdamHyper& h,
                       const StepScalars& s) {
   g *= s.clip;
   m = fmaf(h.b1, m, h.nb1 * g);
   v = fmaf(h.b2, v, h.nb2 * g * g);
-  p = step_param(p, m, sqrt_fast(v), h, s);
+  p = fmaf(-s.rate, m * rcp_fast(fmaf(sqrt_fast(v), s.root, h.eps)), p * s.decay);
 }
+
+// Two floats for the packed fp32 instructions, each half rounded to nearest by
+// itself: half the issue slots, and under the power cap the step's speed goes by
+// its instructions.
+using Pair = unsigned long long;
+MOE_DEV Pair pair(float lo, float hi) {
+  Pair r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+  return r;
+}
+MOE_DEV float2 halves(Pair p) {
+  float2 r;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(p));
+  return r;
+}
+MOE_DEV Pair mul(Pair a, Pair b) {
+  Pair r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+MOE_DEV Pair add(Pair a, Pair b) {
+  Pair r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+MOE_DEV Pair fma(Pair a, Pair b, Pair c) {
+  Pair r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+MOE_DEV Pair both(float v) { return pair(v, v); }
 
 // The moments that are about to be rounded to 8 bits; v goes from sqrt(v) to v.
 // A code is a step of 6 to 12 percent, so one that falls on the other side of a
 // rounding border moves the next step visibly: every product and sum here is
 // rounded by itself, as the formula is written, and the codes do not depend on
 // how a compiler contracts it.
-MOE_DEV void moments8(float g, float& m, float& v, const AdamHyper& h, const StepScalars& s) {
-  g = __fmul_rn(g, s.clip);
-  m = __fadd_rn(__fmul_rn(h.b1, m), __fmul_rn(h.nb1, g));
-  v = __fadd_rn(__fmul_rn(h.b2, __fmul_rn(v, v)), __fmul_rn(__fmul_rn(h.nb2, g), g));
+MOE_DEV void moments8(Pair g, Pair& m, Pair& v, const AdamHyper& h, const StepScalars& s) {
+  g = mul(g, both(s.clip));
+  m = add(mul(both(h.b1), m), mul(both(h.nb1), g));
+  v = add(mul(both(h.b2), mul(v, v)), mul(mul(both(h.nb2), g), g));
 }
 
 // sqrt(v) for v >= kSmallV: one Heron step, r - (r^2 - v) / (2 r), on the hardware's
 // approximation, its residual exact in the fused product.  The step's own error is
 // below 2^-42, so the result is the rounded root but for one value in 2^18.
 constexpr float kSmallV = 1e-36f;
-MOE_DEV float root_heron(float v) {
-  float y;
-  asm("rsqrt.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(v));
-  const float r = v * y;
-  return fmaf(fmaf(-r, r, v), 0.5f * y, r);
+MOE_DEV Pair root_heron(Pair v) {
+  const float2 f = halves(v);
+  float2 y;
+  asm("rsqrt.approx.ftz.f32 %0, %1;" : "=f"(y.x) : "f"(f.x));
+  asm("rsqrt.approx.ftz.f32 %0, %1;" : "=f"(y.y) : "f"(f.y));
+  const Pair yy = pair(y.x, y.y);
+  const Pair r = mul(v, yy);
+  // (v - r r) y / 2 + r
+  return fma(fma(mul(r, both(-1.0f)), r, v), mul(yy, both(0.5f)), r);
 }
 
 // a / b rounded to nearest from inv = 1 / b rounded to nearest (Markstein, "Computation
 // of elementary functions on the IBM RISC System/6000 processor", 1990): one
 // reciprocal serves a whole block.  Exact while a's residual is representable,
 // a > 1e-31; below that the codes may be off by one.
-MOE_DEV float quotient(float a, float b, float inv) {
-  const float q = a * inv;
-  return fmaf(fmaf(-q, b, a), inv, q);
+MOE_DEV Pair quotient(Pair a, float b, float inv) {
+  const Pair q = mul(a, both(inv));
+  return fma(fma(q, both(-b), a), both(inv), q);
+}
+
+MOE_DEV Pair step_param(Pair p, Pair m, Pair r, const AdamHyper& h, const StepScalars& s) {
+  const float2 d = halves(fma(r, both(s.root), both(h.eps)));
+  const Pair u = mul(m, pair(rcp_fast(d.x), rcp_fast(d.y)));
+  return fma(both(-s.rate), u, mul(p, both(s.decay)));
 }
 
 MOE_DEV void load4(const float* p, float (&f)[4]) {
@@ -277,42 +313,46 @@ struct Block8 {
 
   // p, the codes and the scales of the next step
   MOE_DEV void step(const AdamHyper& h, const StepScalars& s) {
-    float m[2][4], r[2][4];
+    Pair m[4], r[4];  // of elements 2 k, 2 k + 1 of the lane's eight
     float least = INFINITY;
 #pragma unroll
     for (int u = 0; u < 2; ++u) {
-      of_e4m3x4(qm[u], m[u]);
-      of_e4m3x4(qv[u], r[u]);
+      float dm[4], dr[4];
+      of_e4m3x4(qm[u], dm);
+      of_e4m3x4(qv[u], dr);
 #pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        m[u][k] *= ms;
-        r[u][k] *= vs;
-        moments8(g[u][k], m[u][k], r[u][k], h, s);
-        least = fminf(least, r[u][k]);
+      for (int k = 0; k < 2; ++k) {
+        Pair& mk = m[2 * u + k];
+        Pair& rk = r[2 * u + k];
+        mk = mul(pair(dm[2 * k], dm[2 * k + 1]), both(ms));
+        rk = mul(pair(dr[2 * k], dr[2 * k + 1]), both(vs));
+        moments8(pair(g[u][2 * k], g[u][2 * k + 1]), mk, rk, h, s);
+        const float2 v = halves(rk);
+        least = fminf(least, fminf(v.x, v.y));
       }
     }
     const bool usual = least >= kSmallV;  // else zeros, or what the approximation would flush
     if (usual) {
 #pragma unroll
-      for (int u = 0; u < 2; ++u)
-#pragma unroll
-        for (int k = 0; k < 4; ++k) r[u][k] = root_heron(r[u][k]);
+      for (int k = 0; k < 4; ++k) r[k] = root_heron(r[k]);
     } else {
 #pragma unroll
-      for (int u = 0; u < 2; ++u)
-#pragma unroll
-        for (int k = 0; k < 4; ++k) r[u][k] = sqrtf(r[u][k]);
+      for (int k = 0; k < 4; ++k) {
+        const float2 v = halves(r[k]);
+        r[k] = pair(sqrtf(v.x), sqrtf(v.y));
+      }
     }
     // magnitudes keep their order as integers, and a NaN is above all of them
     uint32_t bits_m = 0u, bits_r = 0u;
 #pragma unroll
-    for (int u = 0; u < 2; ++u) {
-#pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        p[u][k] = step_param(p[u][k], m[u][k], r[u][k], h, s);
-        bits_m = max(bits_m, __float_as_uint(fabsf(m[u][k])));
-        bits_r = max(bits_r, __float_as_uint(r[u][k]));
-      }
+    for (int k = 0; k < 4; ++k) {
+      float* pk = &p[k / 2][2 * (k % 2)];
+      const float2 np = halves(step_param(pair(pk[0], pk[1]), m[k], r[k], h, s));
+      pk[0] = np.x;
+      pk[1] = np.y;
+      const float2 fm = halves(m[k]), fr = halves(r[k]);
+      bits_m = max(bits_m, max(__float_as_uint(fabsf(fm.x)), __float_as_uint(fabsf(fm.y))));
+      bits_r = max(bits_r, max(__float_as_uint(fr.x), __float_as_uint(fr.y)));
     }
     const float top_m = __uint_as_float(__reduce_max_sync(0xffffffffu, bits_m));
     const float top_r = __uint_as_float(__reduce_max_sync(0xffffffffu, bits_r) & 0x7fffffffu);
@@ -323,14 +363,20 @@ struct Block8 {
     const float ir = vs == 0.f ? 0.f : __frcp_rn(vs);
 #pragma unroll
     for (int u = 0; u < 2; ++u) {
+      float cm[4], cr[4];
 #pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        m[u][k] = quotient(m[u][k], ms, im);
+      for (int k = 0; k < 2; ++k) {
+        const float2 fm = halves(quotient(m[2 * u + k], ms, im));
+        const float2 fr = halves(quotient(r[2 * u + k], vs, ir));
+        const float2 old = halves(r[2 * u + k]);
+        cm[2 * k] = fm.x;
+        cm[2 * k + 1] = fm.y;
         // 2^-9, the smallest code, unless v is 0
-        r[u][k] = fmaxf(quotient(r[u][k], vs, ir), usual || r[u][k] > 0.f ? 0.001953125f : 0.f);
+        cr[2 * k] = fmaxf(fr.x, usual || old.x > 0.f ? 0.001953125f : 0.f);
+        cr[2 * k + 1] = fmaxf(fr.y, usual || old.y > 0.f ? 0.001953125f : 0.f);
       }
-      qm[u] = to_e4m3x4(m[u]);
-      qv[u] = to_e4m3x4(r[u]);
+      qm[u] = to_e4m3x4(cm);
+      qv[u] = to_e4m3x4(cr);
     }
   }
 

@@ -608,6 +608,7 @@ route_kernel(const __grid_constant__ RouteParams p) {
 struct RouteBwdParams {
   int64_t T;
   int E, k;
+  int seg;  // lanes per token: a power of two, >= k and >= E / 8
   int sigmoid, renorm;
   float scale;
   const void* logits;
@@ -617,114 +618,166 @@ struct RouteBwdParams {
   int32_t* status;
 };
 
-MOE_DEV void store_logit(float* p, float v) { *p = v; }
-MOE_DEV void store_logit(__nv_bfloat16* p, float v) { *p = __float2bfloat16_rn(v); }
+template <int W>
+MOE_DEV void store_logits(float* p, const float* v) {
+  if constexpr (W == 4) *reinterpret_cast<float4*>(p) = make_float4(v[0], v[1], v[2], v[3]);
+  else *p = v[0];
+}
+template <int W>
+MOE_DEV void store_logits(__nv_bfloat16* p, const float* v) {
+  if constexpr (W == 4) {
+    __nv_bfloat162 a = __floats2bfloat162_rn(v[0], v[1]), b = __floats2bfloat162_rn(v[2], v[3]);
+    *reinterpret_cast<uint2*>(p) =
+        make_uint2(*reinterpret_cast<uint32_t*>(&a), *reinterpret_cast<uint32_t*>(&b));
+  } else {
+    *p = __float2bfloat16_rn(v[0]);
+  }
+}
 
-// A warp per token; lane j < k holds choice j.  The choices are constants of
-// the gradient.  With a_j = scale * dw_j (summed over equal choices):
-//   softmax:         dh_e = s_e (a_e - sum_i a_i s_i), every expert
-//   softmax, renorm: dh_j = q_j (a_j - sum_i a_i q_i), q = the choices' softmax
-//   sigmoid:         dh_j = a_j s_j (1 - s_j)
-//   sigmoid, renorm: dh_j = q_j (1 - s_j)(a_j - sum_i a_i q_i), q_i = s_i / sum s
-// The dense part of a row is written first and the chosen entries over it, by
-// the same warp.
-template <typename L>
+// `seg` lanes per token: each holds up to 8 entries of the row, lane j < k of
+// them choice j.  The choices are constants of the gradient.  With
+// a_j = scale * dw_j:
+//   DENSE (softmax, not renormalised):  dh_e = s_e (a_e - sum_i a_i s_i)
+//   softmax, renorm:  dh_j = q_j (a_j - sum_i a_i q_i), q = the choices' softmax
+//   sigmoid:          dh_j = a_j s_j (1 - s_j)
+//   sigmoid, renorm:  dh_j = q_j (1 - s_j)(a_j - sum_i a_i q_i), q_i = s_i / sum s
+// What belongs to the chosen entries goes through a row of zeros in shared
+// memory, which the same lanes clear again, so that every entry of dlogits is
+// stored once, in vectors.
+template <typename L, int W, bool DENSE>
 __global__ void __launch_bounds__(kWarps * 32) route_backward_kernel(const RouteBwdParams p) {
+  __shared__ __align__(16) float s_rows[kWarps][256];
   dev::pdl_trigger();
-  dev::pdl_wait();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int64_t nwarps = static_cast<int64_t>(gridDim.x) * kWarps;
-  const bool dense = !p.sigmoid && !p.renorm;
+  const int seg = p.seg, li = lane & (seg - 1), sub = lane / seg;
+  float* row = s_rows[warp] + sub * (seg * 8);
+#pragma unroll
+  for (int i = 0; i < 8; ++i) s_rows[warp][lane + 32 * i] = 0.f;
+  dev::pdl_wait();
+  __syncwarp();
+  constexpr int kParts = 8 / W;  // vectors of W entries: at part * seg * W + li * W
+  const int per_warp = 32 / seg;
+  const int64_t step = static_cast<int64_t>(gridDim.x) * kWarps * per_warp;
   bool bad = false;
-  for (int64_t t = static_cast<int64_t>(blockIdx.x) * kWarps + warp; t < p.T; t += nwarps) {
+  for (int64_t t0 = (static_cast<int64_t>(blockIdx.x) * kWarps + warp) * per_warp; t0 < p.T;
+       t0 += step) {
+    const int64_t t = t0 + sub;
+    const bool live = t < p.T;
     const L* h = static_cast<const L*>(p.logits) + t * p.E;
-    L* out = static_cast<L*>(p.dlogits) + t * p.E;
-    int e = -1;
-    float a = 0.f, x = -INFINITY;
-    if (lane < p.k) {
-      e = __ldg(p.idx + t * p.k + lane);
-      if (e < -1 || e >= p.E) bad = true;
-      if (e < 0 || e >= p.E) e = -1;
-      if (e >= 0) {
-        a = p.scale * __ldg(p.dgate + t * p.k + lane);
-        x = to_float(h[e]);
-        if (!counts(x)) {
-          e = -1;
-          a = 0.f;
-          x = -INFINITY;
+    float v[8];
+    if (DENSE) {
+#pragma unroll
+      for (int c = 0; c < kParts; ++c) {
+        const int o = (c * seg + li) * W;
+        if (live && o < p.E) {
+          load_logits<W>(h + o, v + c * W);
+        } else {
+#pragma unroll
+          for (int i = 0; i < W; ++i) v[c * W + i] = -INFINITY;
         }
       }
     }
-    float d = 0.f;
-    if (dense) {
+    int e = -1;
+    float a = 0.f, x = -INFINITY;
+    if (live && li < p.k) {
+      e = __ldg(p.idx + t * p.k + li);
+      a = p.scale * __ldg(p.dgate + t * p.k + li);
+      if (e < -1 || e >= p.E) {
+        bad = true;
+        e = -1;
+      }
+      if (e >= 0) x = to_float(h[e]);
+      if (!counts(x)) e = -1;
+      if (e < 0) {
+        a = 0.f;
+        x = -INFINITY;
+      }
+    }
+    float dot = 0.f, inv = 0.f, mine = 0.f;  // mine: what this choice adds to its entry
+    if (DENSE) {
       float m = -INFINITY;
-      float v[8];
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
-        const int o = lane + 32 * i;
-        v[i] = o < p.E ? to_float(h[o]) : -INFINITY;
-        if (!counts(v[i])) v[i] = -INFINITY;
+        v[i] = counts(v[i]) ? v[i] : -INFINITY;
         m = fmaxf(m, v[i]);
       }
-      m = warp_max(m);
+      m = seg_max(m, seg);
       float sum = 0.f;
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
         v[i] = v[i] > -INFINITY ? expf(v[i] - m) : 0.f;
         sum += v[i];
       }
-      sum = warp_sum(sum);
-      const float inv = sum > 0.f ? 1.0f / sum : 0.f;
-      const float s = e >= 0 ? expf(x - m) * inv : 0.f;
-      const float dot = warp_sum(a * s);
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const int o = lane + 32 * i;
-        if (o < p.E) store_logit(out + o, -(v[i] * inv) * dot);
-      }
-      float all = 0.f;  // a summed over choices of the same expert
-      for (int j = 0; j < p.k; ++j) {
-        const float aj = __shfl_sync(kFull, a, j);
-        if (__shfl_sync(kFull, e, j) == e) all += aj;
-      }
-      d = s * (all - dot);
+      sum = seg_sum(sum, seg);
+      inv = sum > 0.f ? 1.0f / sum : 0.f;
+      dot = seg_sum(e >= 0 ? a * (expf(x - m) * inv) : 0.f, seg);
+      mine = a;
     } else {
-      for (int o = lane; o < p.E; o += 32) store_logit(out + o, 0.f);
       float s = 0.f, slope = 1.f;
-      const float mx = warp_max(x);
       if (p.sigmoid) {
-        const float ref = p.renorm ? fminf(mx, 0.f) : 0.f;
+        const float mx = p.renorm ? fminf(seg_max(x, seg), 0.f) : 0.f;
         if (e >= 0) {
-          s = x >= 0.f ? 1.0f / (1.0f + expf(-x)) : expf(x - ref) / (1.0f + expf(x));
-          slope = x >= 0.f ? expf(-x) / (1.0f + expf(-x)) : 1.0f / (1.0f + expf(x));
+          const float z = expf(-fabsf(x));  // 1 / (1 + z) and z / (1 + z) are s and 1 - s
+          const float big = __fdividef(1.0f, 1.0f + z), small = __fdividef(z, 1.0f + z);
+          s = x >= 0.f ? big : expf(x - mx) * big;
+          slope = x >= 0.f ? small : big;
         }
-      } else if (e >= 0) {
-        s = expf(x - mx);
-      }
-      float part = 0.f;
-      if (p.renorm) {
-        const float sum = warp_sum(s);
-        s = sum > 0.f ? s / sum : 0.f;
-        const float dot = warp_sum(a * s);
-        part = s * slope * (a - dot);
       } else {
-        part = a * s * slope;
+        const float mx = seg_max(x, seg);
+        if (e >= 0) s = expf(x - mx);
       }
-      for (int j = 0; j < p.k; ++j) {  // choices of the same expert add up
-        const float pj = __shfl_sync(kFull, part, j);
-        if (__shfl_sync(kFull, e, j) == e) d += pj;
+      if (p.renorm) {
+        const float sum = seg_sum(s, seg);
+        s = sum > 0.f ? __fdividef(s, sum) : 0.f;
+        dot = seg_sum(a * s, seg);
+      }
+      mine = s * slope * (a - dot);
+    }
+    // choices of the same expert (a caller's own indices) add up, in order
+    const unsigned same = __match_any_sync(kFull, e >= 0 ? (sub << 9) | e : -1 - lane);
+    if (__any_sync(kFull, __popc(same) > 1)) {
+      float all = 0.f;
+      for (int j = 0; j < p.k; ++j) {
+        const int from = (lane & ~(seg - 1)) + j;
+        const float o = __shfl_sync(kFull, mine, from);
+        if ((same >> from) & 1u) all += o;
+      }
+      mine = all;
+    }
+    if (e >= 0) row[e] = mine;
+    __syncwarp();
+#pragma unroll
+    for (int c = 0; c < kParts; ++c) {
+      const int o = (c * seg + li) * W;
+      if (live && o < p.E) {
+        float r[W];
+        if constexpr (W == 4) {
+          const float4 q = *reinterpret_cast<const float4*>(row + o);
+          r[0] = q.x; r[1] = q.y; r[2] = q.z; r[3] = q.w;
+        } else {
+          r[0] = row[o];
+        }
+        if (DENSE) {
+#pragma unroll
+          for (int i = 0; i < W; ++i) r[i] = (v[c * W + i] * inv) * (r[i] - dot);
+        }
+        store_logits<W>(static_cast<L*>(p.dlogits) + t * p.E + o, r);
       }
     }
-    __syncwarp();  // the row's dense part is written before its chosen entries
-    if (e >= 0) store_logit(out + e, d);
+    __syncwarp();
+    if (e >= 0) row[e] = 0.f;
+    __syncwarp();
   }
   if (__any_sync(kFull, bad) && lane == 0 && p.status) atomicOr(p.status, MOE_STATUS_BAD_INDEX);
 }
 
-unsigned token_grid(int64_t T, int blocks_per_sm) {
-  const int64_t want = (T + kWarps - 1) / kWarps;
-  const int64_t most = static_cast<int64_t>(num_sms()) * blocks_per_sm;
-  return static_cast<unsigned>(want < most ? want : most);
+template <typename L, int W>
+void launch_route_backward_t(const RouteBwdParams& p, cudaStream_t s) {
+  const int64_t per_block = static_cast<int64_t>(kWarps) * (32 / p.seg);
+  const int64_t want = (p.T + per_block - 1) / per_block, most = static_cast<int64_t>(num_sms()) * 8;
+  const dim3 grid(static_cast<unsigned>(want < most ? want : most)), block(kWarps * 32);
+  if (!p.sigmoid && !p.renorm) launch_pdl(route_backward_kernel<L, W, true>, grid, block, 0, s, p);
+  else launch_pdl(route_backward_kernel<L, W, false>, grid, block, 0, s, p);
 }
 
 template <typename L, int V, int W>
@@ -809,11 +862,16 @@ int32_t launch_route_backward(const moe_route_config& c, const void* logits,
   p.dgate = dgate;
   p.dlogits = dlogits;
   p.status = status;
-  const unsigned grid = token_grid(c.T, 8);
-  if (c.dtype == MOE_DTYPE_BF16)
-    launch_pdl(route_backward_kernel<__nv_bfloat16>, dim3(grid), dim3(kWarps * 32), 0, s, p);
-  else
-    launch_pdl(route_backward_kernel<float>, dim3(grid), dim3(kWarps * 32), 0, s, p);
+  p.seg = 1;
+  while (p.seg < c.k || p.seg * 8 < c.E) p.seg <<= 1;
+  const bool vec = c.E % 4 == 0;
+  if (c.dtype == MOE_DTYPE_BF16) {
+    if (vec) launch_route_backward_t<__nv_bfloat16, 4>(p, s);
+    else launch_route_backward_t<__nv_bfloat16, 1>(p, s);
+  } else {
+    if (vec) launch_route_backward_t<float, 4>(p, s);
+    else launch_route_backward_t<float, 1>(p, s);
+  }
   return check_launch("route_backward_kernel");
 }
 
