@@ -441,8 +441,9 @@ int32_t moe_assign(const moe_config* cfg, const int32_t* expert_idx, int32_t* sl
   MOE_TRY(need_ptr4(arrivals, "arrivals"));
   MOE_TRY(need_ptr4(kept_cnt, "kept_cnt"));
   MOE_TRY(need_ptr4(n_dropped, "n_dropped"));
-  return launch_assign(*cfg, expert_idx, slot, kept, tok_of_row, arrivals, kept_cnt, n_dropped,
-                       nullptr, status, reinterpret_cast<cudaStream_t>(stream));
+  (void)status;
+  return launch_assign_choices(*cfg, expert_idx, slot, kept, tok_of_row, arrivals, kept_cnt,
+                               n_dropped, reinterpret_cast<cudaStream_t>(stream));
 }
 
 size_t moe_aux_workspace_size(const moe_config* cfg) {

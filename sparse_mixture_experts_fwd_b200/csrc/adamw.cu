@@ -51,6 +51,7 @@ struct AdamTensor {
 
 struct AdamHyper {
   float b1, nb1, b2, nb2, eps;      // nb = 1 - b, rounded from the double
+  float one;                        // 1 (see add)
   double lr, wd, step;
   double beta1, beta2;
   double max_norm;
@@ -113,17 +114,16 @@ MOE_DEV Pair mul(Pair a, Pair b) {
   asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
   return r;
 }
-MOE_DEV Pair add(Pair a, Pair b) {
-  Pair r;
-  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-  return r;
-}
 MOE_DEV Pair fma(Pair a, Pair b, Pair c) {
   Pair r;
   asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
   return r;
 }
 MOE_DEV Pair both(float v) { return pair(v, v); }
+// a + b, as a * one + b with a 1 that the compiler does not see: it contracts a packed
+// add of a packed product, and a * 1.0f + b just so, into one fused operation in
+// spite of the .rn (found as different last bits of the moments).
+MOE_DEV Pair add(Pair a, Pair b, const AdamHyper& h) { return fma(a, both(h.one), b); }
 
 // The moments that are about to be rounded to 8 bits; v goes from sqrt(v) to v.
 // A code is a step of 6 to 12 percent, so one that falls on the other side of a
@@ -132,8 +132,8 @@ MOE_DEV Pair both(float v) { return pair(v, v); }
 // how a compiler contracts it.
 MOE_DEV void moments8(Pair g, Pair& m, Pair& v, const AdamHyper& h, const StepScalars& s) {
   g = mul(g, both(s.clip));
-  m = add(mul(both(h.b1), m), mul(both(h.nb1), g));
-  v = add(mul(both(h.b2), mul(v, v)), mul(mul(both(h.nb2), g), g));
+  m = add(mul(both(h.b1), m), mul(both(h.nb1), g), h);
+  v = add(mul(both(h.b2), mul(v, v)), mul(mul(both(h.nb2), g), g), h);
 }
 
 // sqrt(v) for v >= kSmallV: one Heron step, r - (r^2 - v) / (2 r), on the hardware's
@@ -731,6 +731,7 @@ extern "C" int32_t moe_adamw_step(const moe_adamw_config* cfg, int32_t n, const 
   h.b2 = static_cast<float>(cfg->beta2);
   h.nb2 = static_cast<float>(1.0 - cfg->beta2);
   h.eps = static_cast<float>(cfg->eps);
+  h.one = 1.0f;
   h.lr = cfg->lr;
   h.wd = cfg->weight_decay;
   h.step = static_cast<double>(cfg->step);

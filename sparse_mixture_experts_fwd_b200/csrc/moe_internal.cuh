@@ -131,6 +131,10 @@ int32_t launch_route(const moe_route_config& c, const void* logits, const float*
 int32_t launch_route_backward(const moe_route_config& c, const void* logits,
                               const int32_t* expert_idx, const float* dgate, void* dlogits,
                               int32_t* status, cudaStream_t s);
+// moe_assign (route.cu): launch_assign, or the whole GPU for long lists
+int32_t launch_assign_choices(const moe_config& c, const int32_t* expert_idx, int32_t* slot,
+                              uint8_t* kept, int32_t* tok_of_row, int32_t* arrivals,
+                              int32_t* kept_cnt, int32_t* n_dropped, cudaStream_t s);
 // the row exchange for up to kMaxChoices choices a token (choices.cu)
 constexpr int kMaxChoices = 16;
 int32_t launch_scatter_choices(const moe_config& c, const void* x, const int32_t* expert_idx,

@@ -333,6 +333,172 @@ __global__ void __launch_bounds__(kAssignThreads, 1) assign_kernel(const AssignA
   }
 }
 
+// The assignment over the whole GPU, for lists that one cluster would walk for long
+// (moe_assign only).  Blocks of kWideChunk choices; three launches:
+//   assign_count:  a block's choices per expert, kept in the block's own part of
+//                  `slot` (its first E entries), which only that block reads later;
+//   assign_scan:   those counts become exclusive prefixes over the blocks, and the
+//                  totals are written;
+//   assign_wide:   slots from the block's prefix, the counts of its earlier warps and
+//                  the rank within the warp, as in assign_kernel.
+constexpr int kWideChunk = 2 * kAssignThreads;  // 2 rounds of 32 a warp
+constexpr int kWideRounds = 3;                  // the last block may take 255 more
+constexpr int64_t kWideFrom = 40 * kWideChunk;  // choices from which it is taken
+
+struct WideArgs {
+  int64_t n_assign;
+  int blocks;
+  int k, E, C;
+  const int32_t* expert_idx;
+  int32_t* slot;
+  uint8_t* kept;
+  int32_t* tok_of_row;
+  int32_t* arrivals;
+  int32_t* kept_cnt;
+  int32_t* n_dropped;
+};
+
+// block b's choices: [first, first + count); the last block takes the rest
+__host__ __device__ __forceinline__ int64_t wide_first(int b) { return static_cast<int64_t>(b) * kWideChunk; }
+__device__ __forceinline__ int wide_count(const WideArgs& p, int b) {
+  return b + 1 < p.blocks ? kWideChunk : static_cast<int>(p.n_assign - wide_first(b));
+}
+
+__global__ void __launch_bounds__(kAssignThreads) assign_count_kernel(const WideArgs p) {
+  __shared__ int s_cnt[256];
+  dev::pdl_trigger();
+  if (threadIdx.x < 256) s_cnt[threadIdx.x] = 0;
+  dev::pdl_wait();
+  __syncthreads();
+  const int b = blockIdx.x, n = wide_count(p, b);
+  const int32_t* idx = p.expert_idx + wide_first(b);
+  int e[kWideRounds];
+#pragma unroll
+  for (int r = 0; r < kWideRounds; ++r) {
+    const int i = r * kAssignThreads + threadIdx.x;
+    e[r] = i < n ? __ldg(idx + i) : -1;
+  }
+#pragma unroll
+  for (int r = 0; r < kWideRounds; ++r)
+    if (e[r] >= 0 && e[r] < p.E) atomicAdd(&s_cnt[e[r]], 1);
+  __syncthreads();
+  if (threadIdx.x < p.E) p.slot[wide_first(b) + threadIdx.x] = s_cnt[threadIdx.x];
+}
+
+// 32 experts (lanes) per block; a warp takes a run of the blocks' counts
+__global__ void __launch_bounds__(kAssignThreads) assign_scan_kernel(const WideArgs p) {
+  __shared__ int s_sum[32][33];
+  dev::pdl_trigger();
+  dev::pdl_wait();
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int e = blockIdx.x * 32 + lane;
+  const int per = (p.blocks + 31) / 32;
+  const int b0 = warp * per, b1 = min(b0 + per, p.blocks);
+  int sum = 0;
+  if (e < p.E) {
+#pragma unroll 4
+    for (int b = b0; b < b1; ++b) sum += p.slot[wide_first(b) + e];
+  }
+  s_sum[warp][lane] = sum;
+  __syncthreads();
+  int before = 0, all = 0;
+#pragma unroll
+  for (int w = 0; w < 32; ++w) {
+    const int v = s_sum[w][lane];
+    before += w < warp ? v : 0;
+    all += v;
+  }
+  if (e >= p.E) return;
+#pragma unroll 4
+  for (int b = b0; b < b1; ++b) {
+    const int64_t at = wide_first(b) + e;
+    const int v = p.slot[at];
+    p.slot[at] = before;
+    before += v;
+  }
+  if (warp == 0) {
+    p.arrivals[e] = all;
+    p.kept_cnt[e] = all < p.C ? all : p.C;
+  }
+}
+
+__global__ void __launch_bounds__(kAssignThreads, 1) assign_wide_kernel(const WideArgs p) {
+  extern __shared__ int s_mem[];
+  const int E = p.E;
+  const int Ep = E | 1;      // odd stride: a column (one expert, all warps) in 32 banks
+  int* s_cnt = s_mem;        // [32 warps][Ep]
+  int* s_base = s_cnt + 32 * Ep;  // [E] earlier blocks' choices
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const unsigned lower = (1u << lane) - 1u;
+  dev::pdl_trigger();
+  for (int i = tid; i < 32 * Ep; i += kAssignThreads) s_cnt[i] = 0;
+  dev::pdl_wait();
+  const int b = blockIdx.x, n = wide_count(p, b);
+  const int64_t first = wide_first(b);
+  for (int x = tid; x < E; x += kAssignThreads) s_base[x] = p.slot[first + x];
+  // a warp's run of consecutive choices, in rounds of 32
+  const int per_warp = (n + 32 * 32 - 1) / (32 * 32) * 32;
+  const int w0 = warp * per_warp, w1 = min(w0 + per_warp, n);
+  int ev[kWideRounds], lv[kWideRounds];
+#pragma unroll
+  for (int r = 0; r < kWideRounds; ++r) {
+    const int i = w0 + 32 * r + lane;
+    ev[r] = i < w1 ? __ldg(p.expert_idx + first + i) : -1;
+    if (ev[r] < 0 || ev[r] >= E) ev[r] = -1;
+  }
+  __syncthreads();  // the counts are zero, and the prefixes read before any slot is written
+#pragma unroll
+  for (int r = 0; r < kWideRounds; ++r) {
+    lv[r] = 0;
+    if (w0 + 32 * r < w1) {  // the same for the whole warp
+      const int e = ev[r];
+      const unsigned peers = __match_any_sync(0xffffffffu, e);
+      const int have = e >= 0 ? s_cnt[warp * Ep + e] : 0;
+      __syncwarp();  // every peer has read the count before the leader moves it
+      if (e >= 0 && lane == __ffs(peers) - 1) s_cnt[warp * Ep + e] = have + __popc(peers);
+      __syncwarp();
+      lv[r] = have + __popc(peers & lower);
+    }
+  }
+  __syncthreads();
+  for (int x = warp; x < E; x += kAssignThreads / 32) {  // exclusive prefix over the warps
+    const int c = s_cnt[lane * Ep + x];
+    int incl = c;
+#pragma unroll
+    for (int off = 1; off < 32; off <<= 1) {
+      const int o = __shfl_up_sync(0xffffffffu, incl, off);
+      if (lane >= off) incl += o;
+    }
+    s_cnt[lane * Ep + x] = incl - c;
+  }
+  __syncthreads();
+#pragma unroll
+  for (int r = 0; r < kWideRounds; ++r) {
+    const int i = w0 + 32 * r + lane;
+    if (i < w1) {
+      const int e = ev[r];
+      const int64_t a = first + i;
+      const int s = e >= 0 ? s_base[e] + s_cnt[warp * Ep + e] + lv[r] : INT_MAX;
+      p.slot[a] = s;
+      const bool kp = e >= 0 && s < p.C;
+      p.kept[a] = kp ? 1 : 0;
+      if (kp) p.tok_of_row[static_cast<int64_t>(e) * p.C + s] = static_cast<int32_t>(a / p.k);
+    }
+  }
+  // the free rows, an expert at a time per warp of the grid, and the dropped total
+  for (int x = b * 32 + warp; x < E; x += static_cast<int>(gridDim.x) * 32) {
+    for (int r = p.kept_cnt[x] + lane; r < p.C; r += 32)
+      p.tok_of_row[static_cast<int64_t>(x) * p.C + r] = -1;
+  }
+  if (b == 0 && warp == 0) {
+    int drop = 0;
+    for (int x = lane; x < E; x += 32) drop += p.arrivals[x] - p.kept_cnt[x];
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) drop += __shfl_xor_sync(0xffffffffu, drop, off);
+    if (lane == 0) p.n_dropped[0] = drop;
+  }
+}
+
 // Totals for a call with no choices (T = 0): zero counts, empty row map.
 __global__ void assign_empty_kernel(int E, int C, int32_t* arrivals, int32_t* kept_cnt,
                                     int32_t* n_dropped, int32_t* tok_of_row) {
@@ -492,6 +658,41 @@ int32_t launch_assign(const moe_config& c, const int32_t* expert_idx, int32_t* s
   cfg.numAttrs = 2;
   cudaLaunchKernelEx(&cfg, assign_kernel, p);
   return check_launch("assign_kernel");
+}
+
+// moe_assign: one cluster for short lists, the whole GPU for long ones.  Measured, one
+// against the other (us): 16 k choices 9.4 / 14.3, 131 k 17.4 / 13.9, 524 k (256
+// experts) 76 / 17.4, 1 M 133 / 27.
+int32_t launch_assign_choices(const moe_config& c, const int32_t* expert_idx, int32_t* slot,
+                              uint8_t* kept, int32_t* tok_of_row, int32_t* arrivals,
+                              int32_t* kept_cnt, int32_t* n_dropped, cudaStream_t s) {
+  WideArgs p{};
+  p.n_assign = c.T * c.k;
+  if (p.n_assign < kWideFrom)
+    return launch_assign(c, expert_idx, slot, kept, tok_of_row, arrivals, kept_cnt, n_dropped,
+                         nullptr, nullptr, s);
+  p.blocks = static_cast<int>(p.n_assign / kWideChunk);
+  // a last block needs room for its counts; fewer choices go to the one before
+  if (p.n_assign - wide_first(p.blocks) >= 256) ++p.blocks;
+  p.k = c.k;
+  p.E = c.E;
+  p.C = c.capacity;
+  p.expert_idx = expert_idx;
+  p.slot = slot;
+  p.kept = kept;
+  p.tok_of_row = tok_of_row;
+  p.arrivals = arrivals;
+  p.kept_cnt = kept_cnt;
+  p.n_dropped = n_dropped;
+  const size_t smem = (32 * static_cast<size_t>(c.E | 1) + c.E) * sizeof(int);
+  if (cudaFuncSetAttribute(assign_wide_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                           static_cast<int>((32 * 257 + 256) * sizeof(int))) != cudaSuccess)
+    return check_launch("cudaFuncSetAttribute(assign_wide_kernel)");
+  const dim3 grid(static_cast<unsigned>(p.blocks)), block(kAssignThreads);
+  launch_pdl(assign_count_kernel, grid, block, 0, s, p);
+  launch_pdl(assign_scan_kernel, dim3((c.E + 31) / 32), block, 0, s, p);
+  launch_pdl(assign_wide_kernel, grid, block, smem, s, p);
+  return check_launch("assign_wide_kernel");
 }
 
 }  // namespace moe

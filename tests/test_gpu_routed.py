@@ -328,7 +328,8 @@ ROWS = [
     # T, E, k, C, d
     (1, 4, 3, 1, 64), (5, 128, 4, 5, 768), (37, 16, 8, 20, 128), (300, 9, 5, 100, 192),
     (64, 256, 16, 3, 64), (2000, 32, 3, 150, 64), (11, 3, 1, 4, 320), (50, 8, 2, 9, 2560),
-    (400, 40, 9, 90, 64), (7, 16, 16, 0, 64),
+    (400, 40, 9, 90, 64), (7, 16, 16, 0, 64), (333, 20, 16, 300, 128), (65, 12, 12, 60, 192),
+    (6000, 64, 8, 800, 256), (9500, 32, 4, 1300, 64),
 ]
 
 
@@ -343,22 +344,33 @@ def test_assign(moe, case):
         assert torch.equal(got[name].cpu(), v), name
 
 
-def test_assign_many_choices(moe):
-    """More choices than the assignment holds in registers (its second walk)."""
-    T, E, k, C = 40000, 64, 8, 4000
+@pytest.mark.parametrize("T,E,k,C", [
+    (40000, 64, 8, 4000), (4096, 256, 8, 100), (4095, 256, 8, 200), (8191, 200, 8, 300),
+    (65536 + 31, 7, 1, 70000), (8200, 16, 16, 5000), (2051, 256, 16, 40), (300_000, 256, 8, 0),
+    (50_001, 33, 5, 9000)])
+def test_assign_many_choices(moe, T, E, k, C):
+    """Long lists (several blocks, a last block of its own or merged into the one before)."""
     idx = choices(T, E, k, 1, 0.02)
+    if T % 2:
+        idx[T // 3:2 * T // 3] = idx[0]        # a long run of the same experts
+        idx[5] = E
     got = moe.assign(moe.make_config(T, 64, 64, E, k, C), idx.cuda())
     e = idx.reshape(-1).long()
-    there = e >= 0
+    there = (e >= 0) & (e < E)
     order = torch.argsort(torch.where(there, e, E), stable=True)
     arrivals = torch.bincount(e[there], minlength=E)
     first = torch.cat([torch.zeros(1, dtype=torch.long), arrivals.cumsum(0)[:-1]])
     slot = torch.full((T * k,), 2 ** 31 - 1)
     n = int(there.sum())
     slot[order[:n]] = torch.arange(n) - first[e[order[:n]]]
+    kept = there & (slot < C)
+    tok = torch.full((E * C,), -1)
+    tok[(e * C + slot)[kept]] = (torch.arange(T * k) // k)[kept]
     assert torch.equal(got["slot"].cpu().view(-1).long(), slot)
     assert torch.equal(got["arrivals"].cpu().long(), arrivals)
-    assert torch.equal(got["kept"].cpu().view(-1).bool(), there & (slot < C))
+    assert torch.equal(got["kept_cnt"].cpu().long(), arrivals.clamp(max=C))
+    assert torch.equal(got["kept"].cpu().view(-1).bool(), kept)
+    assert torch.equal(got["tok_of_row"].cpu().long(), tok)
     assert int(got["n_dropped"]) == int((arrivals - C).clamp(min=0).sum())
 
 
