@@ -344,6 +344,8 @@ __global__ void __launch_bounds__(kAssignThreads, 1) assign_kernel(const AssignA
 constexpr int kWideChunk = 2 * kAssignThreads;  // 2 rounds of 32 a warp
 constexpr int kWideRounds = 3;                  // the last block may take 255 more
 constexpr int64_t kWideFrom = 40 * kWideChunk;  // choices from which it is taken
+constexpr int64_t kOneUpTo = kAssignThreads;  // choices that one block takes
+constexpr int64_t kOneRows = 1 << 16;         // and the rows whose map it writes
 
 struct WideArgs {
   int64_t n_assign;
@@ -422,33 +424,39 @@ __global__ void __launch_bounds__(kAssignThreads) assign_scan_kernel(const WideA
   }
 }
 
+// ONE: a single block has the whole list, a round a warp, and writes the totals
+// itself.
+template <bool ONE>
 __global__ void __launch_bounds__(kAssignThreads, 1) assign_wide_kernel(const WideArgs p) {
+  constexpr int kRounds = ONE ? 1 : kWideRounds;
   extern __shared__ int s_mem[];
   const int E = p.E;
   const int Ep = E | 1;      // odd stride: a column (one expert, all warps) in 32 banks
   int* s_cnt = s_mem;        // [32 warps][Ep]
-  int* s_base = s_cnt + 32 * Ep;  // [E] earlier blocks' choices
+  int* s_base = s_cnt + 32 * Ep;  // [E] earlier blocks' choices; ONE: all choices
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const unsigned lower = (1u << lane) - 1u;
   dev::pdl_trigger();
   for (int i = tid; i < 32 * Ep; i += kAssignThreads) s_cnt[i] = 0;
   dev::pdl_wait();
-  const int b = blockIdx.x, n = wide_count(p, b);
-  const int64_t first = wide_first(b);
-  for (int x = tid; x < E; x += kAssignThreads) s_base[x] = p.slot[first + x];
+  const int b = blockIdx.x;
+  const int n = ONE ? static_cast<int>(p.n_assign) : wide_count(p, b);
+  const int64_t first = ONE ? 0 : wide_first(b);
+  if (!ONE)
+    for (int x = tid; x < E; x += kAssignThreads) s_base[x] = p.slot[first + x];
   // a warp's run of consecutive choices, in rounds of 32
   const int per_warp = (n + 32 * 32 - 1) / (32 * 32) * 32;
   const int w0 = warp * per_warp, w1 = min(w0 + per_warp, n);
-  int ev[kWideRounds], lv[kWideRounds];
+  int ev[kRounds], lv[kRounds];
 #pragma unroll
-  for (int r = 0; r < kWideRounds; ++r) {
+  for (int r = 0; r < kRounds; ++r) {
     const int i = w0 + 32 * r + lane;
     ev[r] = i < w1 ? __ldg(p.expert_idx + first + i) : -1;
     if (ev[r] < 0 || ev[r] >= E) ev[r] = -1;
   }
   __syncthreads();  // the counts are zero, and the prefixes read before any slot is written
 #pragma unroll
-  for (int r = 0; r < kWideRounds; ++r) {
+  for (int r = 0; r < kRounds; ++r) {
     lv[r] = 0;
     if (w0 + 32 * r < w1) {  // the same for the whole warp
       const int e = ev[r];
@@ -470,29 +478,37 @@ __global__ void __launch_bounds__(kAssignThreads, 1) assign_wide_kernel(const Wi
       if (lane >= off) incl += o;
     }
     s_cnt[lane * Ep + x] = incl - c;
+    if (ONE && lane == 31) s_base[x] = incl;
   }
   __syncthreads();
 #pragma unroll
-  for (int r = 0; r < kWideRounds; ++r) {
+  for (int r = 0; r < kRounds; ++r) {
     const int i = w0 + 32 * r + lane;
     if (i < w1) {
       const int e = ev[r];
       const int64_t a = first + i;
-      const int s = e >= 0 ? s_base[e] + s_cnt[warp * Ep + e] + lv[r] : INT_MAX;
+      const int s = e >= 0 ? (ONE ? 0 : s_base[e]) + s_cnt[warp * Ep + e] + lv[r] : INT_MAX;
       p.slot[a] = s;
       const bool kp = e >= 0 && s < p.C;
       p.kept[a] = kp ? 1 : 0;
       if (kp) p.tok_of_row[static_cast<int64_t>(e) * p.C + s] = static_cast<int32_t>(a / p.k);
     }
   }
+  if (ONE) {
+    for (int x = tid; x < E; x += kAssignThreads) {
+      p.arrivals[x] = s_base[x];
+      p.kept_cnt[x] = min(s_base[x], p.C);
+    }
+  }
   // the free rows, an expert at a time per warp of the grid, and the dropped total
   for (int x = b * 32 + warp; x < E; x += static_cast<int>(gridDim.x) * 32) {
-    for (int r = p.kept_cnt[x] + lane; r < p.C; r += 32)
+    for (int r = (ONE ? min(s_base[x], p.C) : p.kept_cnt[x]) + lane; r < p.C; r += 32)
       p.tok_of_row[static_cast<int64_t>(x) * p.C + r] = -1;
   }
   if (b == 0 && warp == 0) {
     int drop = 0;
-    for (int x = lane; x < E; x += 32) drop += p.arrivals[x] - p.kept_cnt[x];
+    for (int x = lane; x < E; x += 32)
+      drop += ONE ? max(s_base[x] - p.C, 0) : p.arrivals[x] - p.kept_cnt[x];
 #pragma unroll
     for (int off = 16; off > 0; off >>= 1) drop += __shfl_xor_sync(0xffffffffu, drop, off);
     if (lane == 0) p.n_dropped[0] = drop;
@@ -660,20 +676,19 @@ int32_t launch_assign(const moe_config& c, const int32_t* expert_idx, int32_t* s
   return check_launch("assign_kernel");
 }
 
-// moe_assign: one cluster for short lists, the whole GPU for long ones.  Measured, one
-// against the other (us): 16 k choices 9.4 / 14.3, 131 k 17.4 / 13.9, 524 k (256
-// experts) 76 / 17.4, 1 M 133 / 27.
+// moe_assign: one block for short lists, one cluster for longer ones, the whole GPU
+// for long ones.  Measured, one against the other (us): block / cluster 512 choices
+// 3.9 / 5.1, 4096 8.7 / 5.8; cluster / GPU 16 k 9.4 / 14.3, 131 k 17.4 / 13.9,
+// 524 k (256 experts) 76 / 17.4, 1 M 133 / 27.
 int32_t launch_assign_choices(const moe_config& c, const int32_t* expert_idx, int32_t* slot,
                               uint8_t* kept, int32_t* tok_of_row, int32_t* arrivals,
                               int32_t* kept_cnt, int32_t* n_dropped, cudaStream_t s) {
   WideArgs p{};
   p.n_assign = c.T * c.k;
-  if (p.n_assign < kWideFrom)
+  const bool one = p.n_assign > 0 && p.n_assign <= kOneUpTo && int64_t(c.E) * c.capacity <= kOneRows;
+  if (!one && p.n_assign < kWideFrom)
     return launch_assign(c, expert_idx, slot, kept, tok_of_row, arrivals, kept_cnt, n_dropped,
                          nullptr, nullptr, s);
-  p.blocks = static_cast<int>(p.n_assign / kWideChunk);
-  // a last block needs room for its counts; fewer choices go to the one before
-  if (p.n_assign - wide_first(p.blocks) >= 256) ++p.blocks;
   p.k = c.k;
   p.E = c.E;
   p.C = c.capacity;
@@ -685,13 +700,18 @@ int32_t launch_assign_choices(const moe_config& c, const int32_t* expert_idx, in
   p.kept_cnt = kept_cnt;
   p.n_dropped = n_dropped;
   const size_t smem = (32 * static_cast<size_t>(c.E | 1) + c.E) * sizeof(int);
-  if (cudaFuncSetAttribute(assign_wide_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                           static_cast<int>((32 * 257 + 256) * sizeof(int))) != cudaSuccess)
-    return check_launch("cudaFuncSetAttribute(assign_wide_kernel)");
-  const dim3 grid(static_cast<unsigned>(p.blocks)), block(kAssignThreads);
+  const dim3 block(kAssignThreads);
+  if (one) {
+    launch_pdl(assign_wide_kernel<true>, dim3(1), block, smem, s, p);
+    return check_launch("assign_wide_kernel");
+  }
+  p.blocks = static_cast<int>(p.n_assign / kWideChunk);
+  // a last block needs room for its counts; fewer choices go to the one before
+  if (p.n_assign - wide_first(p.blocks) >= 256) ++p.blocks;
+  const dim3 grid(static_cast<unsigned>(p.blocks));
   launch_pdl(assign_count_kernel, grid, block, 0, s, p);
   launch_pdl(assign_scan_kernel, dim3((c.E + 31) / 32), block, 0, s, p);
-  launch_pdl(assign_wide_kernel, grid, block, smem, s, p);
+  launch_pdl(assign_wide_kernel<false>, grid, block, smem, s, p);
   return check_launch("assign_wide_kernel");
 }
 

@@ -345,7 +345,7 @@ def test_assign(moe, case):
 
 
 @pytest.mark.parametrize("T,E,k,C", [
-    (40000, 64, 8, 4000), (4096, 256, 8, 100), (4095, 256, 8, 200), (8191, 200, 8, 300),
+    (128, 256, 8, 4), (1024, 9, 1, 200), (73, 16, 14, 30000), (40000, 64, 8, 4000), (4096, 256, 8, 100), (4095, 256, 8, 200), (8191, 200, 8, 300),
     (65536 + 31, 7, 1, 70000), (8200, 16, 16, 5000), (2051, 256, 16, 40), (300_000, 256, 8, 0),
     (50_001, 33, 5, 9000)])
 def test_assign_many_choices(moe, T, E, k, C):
