@@ -275,15 +275,16 @@ def dispatch(cfg, x, expert_idx, slot, kept, xe=None, status=None, stream=None):
 
 def _arg(t, name, dtype, shape):
     """Device pointer of an argument whose dtype, shape and device are settled."""
-    if t.dtype != dtype:
+    if t.dtype is dtype and t.shape == shape and t.is_cuda and t.is_contiguous() and \
+            t.get_device() == torch._C._cuda_getDevice():
+        return t.data_ptr()
+    if t.dtype is not dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
     if t.shape != shape:
         raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
-    p = _ptr(t, name)
-    if t.get_device() != torch._C._cuda_getDevice():
-        raise ValueError(f"{name} is on {t.device}, the current device is "
-                         f"cuda:{torch.cuda.current_device()}")
-    return p
+    _ptr(t, name)
+    raise ValueError(f"{name} is on {t.device}, the current device is "
+                     f"cuda:{torch.cuda.current_device()}")
 
 
 def _empty(shape, dtype, device, stream):

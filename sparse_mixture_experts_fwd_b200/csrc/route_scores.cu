@@ -385,6 +385,100 @@ MOE_DEV void make_keys(const RouteParams& p, const float (&x)[V], const float (&
   }
 }
 
+// Whether keys that are close have unlike inputs: equal logits (and biases) are
+// in their order already.  close: this lane's choice (at `rel`) and the next;
+// edge: the last choice and one of those this lane has left.
+template <typename L, int V>
+MOE_DEV void check_inputs(const RouteParams& p, const L* h, bool has_bias, unsigned near,
+                          uint32_t mine, int rel, uint32_t last, KeyList<V> list, bool& close,
+                          bool& edge) {
+  const bool there = rel >= 0 && rel < p.k && mine != 0u;
+  const int e = there ? expert_of(mine) : 0;
+  const float x = there ? to_float(h[e]) : 0.f, b = there && has_bias ? __ldg(p.bias + e) : 0.f;
+  const float xa = __shfl_down_sync(kFull, x, 1), ba = __shfl_down_sync(kFull, b, 1);
+  close = close && !(x == xa && b == ba);
+  if (edge) {
+    const int el = expert_of(last);
+    const float xl = to_float(h[el]), bl = has_bias ? __ldg(p.bias + el) : 0.f;
+    edge = false;
+    while (list.head != 0u && (last >> 9) - (list.head >> 9) <= near) {
+      const int en = expert_of(list.head);
+      edge |= to_float(h[en]) != xl || (has_bias && __ldg(p.bias + en) != bl);
+      list.take(list.head);
+    }
+  }
+}
+
+// The order of the choices in fp64, where the groups are settled: the k choices and
+// those left that are close to the last one, a candidate per lane, ranked by
+// counting.  False if there are more candidates than lanes.
+template <typename L, int V, int MODE>
+MOE_DEV bool settle_order(const RouteParams& p, const L* h, bool has_bias, unsigned near, int at,
+                          uint32_t last, KeyList<V> list, uint32_t& mine) {
+  const int lane = threadIdx.x & 31;
+  uint32_t cand = __shfl_sync(kFull, mine, (at + lane) & 31);
+  if (lane >= p.k) cand = 0u;
+  int n = p.k;
+  for (;; ++n) {
+    const uint32_t next = __reduce_max_sync(kFull, list.head);
+    if (next == 0u || (last >> 9) - (next >> 9) > near) break;
+    if (n == 32) return false;
+    if (lane == n) cand = next;
+    list.take(next);
+  }
+  const int e = expert_of(cand);
+  double c = -INFINITY;
+  if (cand != 0u) {
+    const double x = to_float(h[e]);
+    c = MODE == kByLogit ? x : 1.0 / (1.0 + exp(-x)) + (has_bias ? __ldg(p.bias + e) : 0.f);
+  }
+  int rank = 0;
+  for (int i = 0; i < n; ++i) {
+    const double o = __shfl_sync(kFull, c, i);
+    const int oe = __shfl_sync(kFull, e, i);
+    rank += o > c || (o == c && oe < e);
+  }
+  for (int i = 0; i < n; ++i) {
+    const int r = __shfl_sync(kFull, rank, i);
+    const uint32_t key = __shfl_sync(kFull, cand, i);
+    if (r < p.k && lane == at + r) mine = key;
+  }
+  return true;
+}
+
+// Which groups stay, in fp64.  a1, a2: the keys of the group's two best.  False
+// where a third candidate is so close to them that they are not known.
+template <typename L, int V, int MODE>
+MOE_DEV bool settle_groups(const RouteParams& p, const L* h, bool has_bias, unsigned near, int q,
+                           uint32_t a1, uint32_t a2, const uint32_t (&key)[V], bool& out) {
+  const uint32_t least = p.group_top == 2 ? a2 : a1;
+  bool third = false;
+#pragma unroll
+  for (int i = 0; i < (V < 3 ? V : 3); ++i)
+    third |= key[i] != 0u && key[i] != a1 && key[i] != a2 && (least >> 9) - (key[i] >> 9) <= near;
+  if (__any_sync(kFull, third)) return false;
+  double v[2];
+#pragma unroll 1
+  for (int i = 0; i < 2; ++i) {
+    const uint32_t a = i == 0 ? a1 : a2;
+    const int e = expert_of(a);
+    double c = -INFINITY;
+    if (a != 0u) {
+      const double x = to_float(h[e]);
+      c = MODE == kByLogit ? x : 1.0 / (1.0 + exp(-x)) + (has_bias ? __ldg(p.bias + e) : 0.f);
+    }
+    v[i] = c;
+  }
+  const double value = p.group_top == 2 ? v[0] + v[1] : fmax(v[0], v[1]);
+  int rank = 0;
+  for (int g = 0; g < p.G; ++g) {
+    const double o = __shfl_sync(kFull, value, g * p.lanes);
+    rank += o > value || (o == value && g < q);
+  }
+  out = q < p.G && rank >= p.top_groups;
+  return true;
+}
+
 // A warp per token.  Lane l holds V logits of one group (of the whole row
 // where there is no group limit).  Each candidate becomes a 32-bit key,
 // (value in 23 bits) << 9 | (255 - expert): unique, larger is better, equal
@@ -394,8 +488,11 @@ MOE_DEV void make_keys(const RouteParams& p, const float (&x)[V], const float (&
 // sorts its keys once, and each choice is one warp-wide integer maximum over the
 // lanes' first keys.  The rounding is checked afterwards: where neighbours in
 // the order (or the last choice and one left out) are within near_units, and
-// are not equal inputs, the token is left open and the block's warps decide
-// the open ones in fp64 at the end (finish_exact), side by side.
+// are not equal inputs, those candidates alone are ranked in fp64
+// (settle_order, settle_groups).  What that leaves open (softmax scores with a
+// bias, whose sum is needed in fp64 too; a third candidate close to a group's
+// two) is listed, and the block's warps decide it at the end (finish_exact),
+// side by side.
 //
 // The scores here only decide, so they take the hardware's exp2 and reciprocal;
 // the weights of the k choices are formed from their logits with expf.  That
@@ -529,11 +626,19 @@ route_kernel(const __grid_constant__ RouteParams p) {
           last = __reduce_max_sync(kFull, g);
           if (g == last) g = 0u;
         }
-        if (g != 0u) {
-          // a group left out that may be as good as the last one that stays
-          if (!kExactKey && (last >> 5) - (g >> 5) <= 2 * kNear) unsure = true;
-          key[0] = 0u;  // the list behind a 0 is never reached
+        bool out = g != 0u;
+        // a group left out that may be as good as the last one that stays
+        const bool near_out = !kExactKey && out && (last >> 5) - (g >> 5) <= 2 * kNear;
+        if (__any_sync(kFull, near_out || unsure)) {
+          unsure = __any_sync(kFull, unsure);
+          if constexpr (MODE != kBySoftmax && !kExactKey) {
+            const L* h = rows + static_cast<int64_t>(done + slot) * p.E;
+            unsure = unsure || !settle_groups<L, V, MODE>(p, h, has_bias, kNear, q, a1, a2, key, out);
+          } else {
+            unsure = true;
+          }
         }
+        if (out) key[0] = 0u;  // the list behind a 0 is never reached
       }
 
       KeyList<V> list;
@@ -546,15 +651,20 @@ route_kernel(const __grid_constant__ RouteParams p) {
         if (rel == j) mine = last;
         list.take(last);
       }
-      // the last choice against what this lane has left: close, and not the same inputs
-      if (!kExactKey && list.head != 0u && (last >> 9) - (list.head >> 9) <= kNear) {
-        const L* h = rows + static_cast<int64_t>(done + slot) * p.E;
-        const int el = expert_of(last);
-        const float xl = to_float(h[el]), bl = has_bias ? __ldg(p.bias + el) : 0.f;
-        while (list.head != 0u && (last >> 9) - (list.head >> 9) <= kNear) {
-          const int en = expert_of(list.head);
-          unsure |= to_float(h[en]) != xl || (has_bias && __ldg(p.bias + en) != bl);
-          list.take(list.head);
+      if constexpr (!kExactKey) {
+        // neighbours in the order, and the last choice against what this lane has left
+        const uint32_t after = __shfl_down_sync(kFull, mine, 1);
+        bool close = rel >= 0 && rel + 1 < p.k && after != 0u && (mine >> 9) - (after >> 9) <= kNear;
+        bool edge = list.head != 0u && (last >> 9) - (list.head >> 9) <= kNear;
+        if (__any_sync(kFull, close || edge)) {
+          const L* h = rows + static_cast<int64_t>(done + slot) * p.E;
+          check_inputs(p, h, has_bias, kNear, mine, rel, last, list, close, edge);
+          if (__any_sync(kFull, close || edge)) {
+            bool settled = false;
+            if constexpr (MODE != kBySoftmax)
+              settled = settle_order<L, V, MODE>(p, h, has_bias, kNear, slot * p.seg, last, list, mine);
+            if (!settled) unsure = true;
+          }
         }
       }
       if (__any_sync(kFull, unsure)) open |= 1u << slot;
@@ -568,15 +678,6 @@ route_kernel(const __grid_constant__ RouteParams p) {
     const L* h = rows + static_cast<int64_t>(done) * p.E;
     const int e = in && mine ? expert_of(mine) : -1;
     const float xj = e >= 0 ? to_float(h[my_slot * p.E + e]) : -INFINITY;
-    if constexpr (!kExactKey) {
-      const float bj = e >= 0 && has_bias ? __ldg(p.bias + e) : 0.f;
-      const uint32_t after = __shfl_down_sync(kFull, mine, 1);
-      const float xa = __shfl_down_sync(kFull, xj, 1), ba = __shfl_down_sync(kFull, bj, 1);
-      const bool close = in && my_j + 1 < p.k && after != 0u &&
-                         (mine >> 9) - (after >> 9) <= kNear && !(xj == xa && bj == ba);
-      for (unsigned c = __ballot_sync(kFull, close); c; c &= c - 1u)
-        open |= 1u << ((__ffs(c) - 1) / p.seg);
-    }
     const float w = choice_weight(p, xj, my_m, my_inv);
     if (in && !((open >> my_slot) & 1u)) {
       const int64_t o = (tb + done) * p.k + my_slot * p.k + my_j;

@@ -122,6 +122,35 @@ def test_route_candidates_one_step_apart(moe, score, bias_on):
     check_route(moe, y, 2, None if b is None else b[:16], score=score)
 
 
+@pytest.mark.parametrize("dtype", DTYPES, ids=["f32", "bf16"])
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+def test_route_twins(moe, score, dtype):
+    """Every expert has a twin whose logit is one step of its type away (up, down or equal), and
+    with groups every group has a twin that differs in one expert: few candidates are close, at
+    every place of the order and at its borders."""
+    g = torch.Generator().manual_seed(12)
+    T, E = 150, 64
+    base = (1.2 * torch.randn(T, E // 2, generator=g)).to(dtype)
+    move = torch.randint(-1, 2, (T, E // 2), generator=g)
+    it = torch.int32 if dtype == torch.float32 else torch.int16
+    twin = (base.view(it) + move.to(it)).view(dtype)
+    x = torch.stack([base, twin], dim=2).view(T, E).contiguous()
+    groups = x.view(T, 4, 2, 8)[:, :, :1].expand(T, 4, 2, 8).clone()
+    one = torch.randint(0, 8, (T, 4), generator=g)
+    t, q = torch.arange(T)[:, None], torch.arange(4)[None, :]
+    bumped = (groups[:, :, 1].clone().view(it).gather(2, one[:, :, None])[:, :, 0] + 1).view(dtype)
+    groups[t, q, 1, one] = bumped
+    y = groups.reshape(T, E)[:, torch.randperm(8, generator=g).repeat_interleave(8) * 8
+                             + torch.arange(8).repeat(8)].contiguous()
+    flat = torch.full((E,), 0.015625)
+    for b in (None, flat):
+        for k in (1, 2, 7, 16):
+            check_route(moe, x, k, b, score=score)
+            for gt in (1, 2):
+                check_route(moe, x, min(k, 12), b, score=score, groups=8, top_groups=3, group_top=gt)
+                check_route(moe, y, min(k, 12), b, score=score, groups=8, top_groups=3, group_top=gt)
+
+
 def test_route_border_hidden_behind_equal_ones(moe):
     """Many exactly equal candidates at the last place, and one that differs from them by less
     than fp32 shows (its bias makes up for a smaller logit)."""
