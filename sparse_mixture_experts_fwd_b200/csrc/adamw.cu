@@ -95,35 +95,19 @@ MOE_DEV void adam_one(float& p, float g, float& m, float& v, const AdamHyper& h,
   p = fmaf(-s.rate, m * rcp_fast(fmaf(sqrt_fast(v), s.root, h.eps)), p * s.decay);
 }
 
-// Two floats for the packed fp32 instructions, each half rounded to nearest by
-// itself: half the issue slots, and under the power cap the step's speed goes by
-// its instructions.
-using Pair = unsigned long long;
-MOE_DEV Pair pair(float lo, float hi) {
-  Pair r;
-  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
-  return r;
-}
-MOE_DEV float2 halves(Pair p) {
-  float2 r;
-  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(p));
-  return r;
-}
-MOE_DEV Pair mul(Pair a, Pair b) {
-  Pair r;
-  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-  return r;
-}
-MOE_DEV Pair fma(Pair a, Pair b, Pair c) {
-  Pair r;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
-  return r;
-}
-MOE_DEV Pair both(float v) { return pair(v, v); }
+// (packed arithmetic: half the issue slots, and under the power cap the step's speed
+// goes by its instructions)
+using dev::Pair;
+using dev::both;
+using dev::fma2;
+using dev::halves;
+using dev::mul2;
+using dev::pair;
+
 // a + b, as a * one + b with a 1 that the compiler does not see: it contracts a packed
 // add of a packed product, and a * 1.0f + b just so, into one fused operation in
 // spite of the .rn (found as different last bits of the moments).
-MOE_DEV Pair add(Pair a, Pair b, const AdamHyper& h) { return fma(a, both(h.one), b); }
+MOE_DEV Pair add(Pair a, Pair b, const AdamHyper& h) { return fma2(a, both(h.one), b); }
 
 // The moments that are about to be rounded to 8 bits; v goes from sqrt(v) to v.
 // A code is a step of 6 to 12 percent, so one that falls on the other side of a
@@ -131,9 +115,9 @@ MOE_DEV Pair add(Pair a, Pair b, const AdamHyper& h) { return fma(a, both(h.one)
 // rounded by itself, as the formula is written, and the codes do not depend on
 // how a compiler contracts it.
 MOE_DEV void moments8(Pair g, Pair& m, Pair& v, const AdamHyper& h, const StepScalars& s) {
-  g = mul(g, both(s.clip));
-  m = add(mul(both(h.b1), m), mul(both(h.nb1), g), h);
-  v = add(mul(both(h.b2), mul(v, v)), mul(mul(both(h.nb2), g), g), h);
+  g = mul2(g, both(s.clip));
+  m = add(mul2(both(h.b1), m), mul2(both(h.nb1), g), h);
+  v = add(mul2(both(h.b2), mul2(v, v)), mul2(mul2(both(h.nb2), g), g), h);
 }
 
 // sqrt(v) for v >= kSmallV: one Heron step, r - (r^2 - v) / (2 r), on the hardware's
@@ -146,9 +130,9 @@ MOE_DEV Pair root_heron(Pair v) {
   asm("rsqrt.approx.ftz.f32 %0, %1;" : "=f"(y.x) : "f"(f.x));
   asm("rsqrt.approx.ftz.f32 %0, %1;" : "=f"(y.y) : "f"(f.y));
   const Pair yy = pair(y.x, y.y);
-  const Pair r = mul(v, yy);
+  const Pair r = mul2(v, yy);
   // (v - r r) y / 2 + r
-  return fma(fma(mul(r, both(-1.0f)), r, v), mul(yy, both(0.5f)), r);
+  return fma2(fma2(mul2(r, both(-1.0f)), r, v), mul2(yy, both(0.5f)), r);
 }
 
 // a / b rounded to nearest from inv = 1 / b rounded to nearest (Markstein, "Computation
@@ -156,14 +140,14 @@ MOE_DEV Pair root_heron(Pair v) {
 // reciprocal serves a whole block.  Exact while a's residual is representable,
 // a > 1e-31; below that the codes may be off by one.
 MOE_DEV Pair quotient(Pair a, float b, float inv) {
-  const Pair q = mul(a, both(inv));
-  return fma(fma(q, both(-b), a), both(inv), q);
+  const Pair q = mul2(a, both(inv));
+  return fma2(fma2(q, both(-b), a), both(inv), q);
 }
 
 MOE_DEV Pair step_param(Pair p, Pair m, Pair r, const AdamHyper& h, const StepScalars& s) {
-  const float2 d = halves(fma(r, both(s.root), both(h.eps)));
-  const Pair u = mul(m, pair(rcp_fast(d.x), rcp_fast(d.y)));
-  return fma(both(-s.rate), u, mul(p, both(s.decay)));
+  const float2 d = halves(fma2(r, both(s.root), both(h.eps)));
+  const Pair u = mul2(m, pair(rcp_fast(d.x), rcp_fast(d.y)));
+  return fma2(both(-s.rate), u, mul2(p, both(s.decay)));
 }
 
 MOE_DEV void load4(const float* p, float (&f)[4]) {
@@ -324,8 +308,8 @@ struct Block8 {
       for (int k = 0; k < 2; ++k) {
         Pair& mk = m[2 * u + k];
         Pair& rk = r[2 * u + k];
-        mk = mul(pair(dm[2 * k], dm[2 * k + 1]), both(ms));
-        rk = mul(pair(dr[2 * k], dr[2 * k + 1]), both(vs));
+        mk = mul2(pair(dm[2 * k], dm[2 * k + 1]), both(ms));
+        rk = mul2(pair(dr[2 * k], dr[2 * k + 1]), both(vs));
         moments8(pair(g[u][2 * k], g[u][2 * k + 1]), mk, rk, h, s);
         const float2 v = halves(rk);
         least = fminf(least, fminf(v.x, v.y));

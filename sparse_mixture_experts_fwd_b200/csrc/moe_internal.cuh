@@ -492,6 +492,31 @@ __host__ __device__ constexpr uint32_t idesc_bf16_f32(int M, int N) {
 }
 
 
+// Two floats for the packed fp32 instructions: one issue slot for both, each half
+// rounded to nearest by itself.
+using Pair = unsigned long long;
+MOE_DEV Pair pair(float lo, float hi) {
+  Pair r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+  return r;
+}
+MOE_DEV Pair both(float v) { return pair(v, v); }
+MOE_DEV float2 halves(Pair p) {
+  float2 r;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(p));
+  return r;
+}
+MOE_DEV Pair mul2(Pair a, Pair b) {
+  Pair r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+MOE_DEV Pair fma2(Pair a, Pair b, Pair c) {
+  Pair r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+
 // GEGLU hidden unit from its gate and linear accumulators (GEMM-1 columns 2i
 // and 2i + 1): GELU(g) * l with GELU(a) = a * Phi(a) = a (1 + erf(a / sqrt 2)) / 2.
 MOE_DEV float geglu(float g, float l) {

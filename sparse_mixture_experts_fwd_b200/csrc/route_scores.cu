@@ -523,6 +523,28 @@ route_kernel(const __grid_constant__ RouteParams p) {
 
   // this lane's experts: first + (i / W) * lanes * W + li * W + i % W within group q
   const int first = q * p.gs;
+  // the warp's tokens: tb .. tb + count - 1
+  const int64_t tb = (static_cast<int64_t>(blockIdx.x) * kWarps + warp) * p.per_warp;
+  const int count = tb < p.T ? static_cast<int>(min(static_cast<int64_t>(p.per_warp), p.T - tb)) : 0;
+  const L* rows = static_cast<const L*>(p.logits) + tb * p.E;
+  const L* from = rows + first + li * W;  // this lane's part of the next row to load
+  bool has[V / W];
+#pragma unroll
+  for (int c = 0; c < V / W; ++c) has[c] = q < p.G && li * W + c * p.lanes * W < p.gs;
+  auto load_row = [&](float (&x)[V]) {
+#pragma unroll
+    for (int c = 0; c < V / W; ++c) {
+      if (has[c]) {
+        load_logits<W>(from + c * p.lanes * W, x + c * W);
+      } else {
+#pragma unroll
+        for (int i = 0; i < W; ++i) x[c * W + i] = -INFINITY;
+      }
+    }
+    from += p.E;
+  };
+  float ahead[V];  // the next token's logits; the first are on their way during the set-up
+  if (count > 0) load_row(ahead);
   float off[V];    // score modes: the bias's part of the key; NaN masks the expert
   float unit = 0.f;
   if constexpr (MODE != kByLogit) {
@@ -556,32 +578,10 @@ route_kernel(const __grid_constant__ RouteParams p) {
   }
   whole = __all_sync(kFull, whole);
 
-  // the warp's tokens: tb .. tb + count - 1
-  const int64_t tb = (static_cast<int64_t>(blockIdx.x) * kWarps + warp) * p.per_warp;
-  const int count = tb < p.T ? static_cast<int>(min(static_cast<int64_t>(p.per_warp), p.T - tb)) : 0;
-  const L* rows = static_cast<const L*>(p.logits) + tb * p.E;
-  const L* from = rows + first + li * W;  // this lane's part of the next row to load
-  bool has[V / W];
-#pragma unroll
-  for (int c = 0; c < V / W; ++c) has[c] = q < p.G && li * W + c * p.lanes * W < p.gs;
-  auto load_row = [&](float (&x)[V]) {
-#pragma unroll
-    for (int c = 0; c < V / W; ++c) {
-      if (has[c]) {
-        load_logits<W>(from + c * p.lanes * W, x + c * W);
-      } else {
-#pragma unroll
-        for (int i = 0; i < W; ++i) x[c * W + i] = -INFINITY;
-      }
-    }
-    from += p.E;
-  };
   const uint32_t column = dev::smem_u32(&s_warp[warp].column[0][lane]);
   // in the weights' part lane slot * seg + j works for choice j of a batch's token `slot`
   const int my_slot = lane / p.seg, my_j = lane & (p.seg - 1);
 
-  float ahead[V];
-  if (count > 0) load_row(ahead);
   for (int done = 0; done < count; done += p.slots) {
     const int in_batch = min(p.slots, count - done);
     uint32_t mine = 0u;
@@ -592,12 +592,11 @@ route_kernel(const __grid_constant__ RouteParams p) {
 #pragma unroll
       for (int i = 0; i < V; ++i) x[i] = ahead[i];
       if (done + slot + 1 < count) load_row(ahead);
-      // 0 unless a logit is masked, NaN or infinite (or above 1.7e38): the product
+      // 0 unless a logit is masked, NaN or infinite (or above 2.3e38): the product
       // overflows for the lowest values too, and inf * 0 is NaN
       float odd = 0.f;
 #pragma unroll
-      for (int i = 0; i < V; ++i)
-        odd = fmaf(MODE == kBySigmoid ? -kLog2e * x[i] : x[i] + x[i], 0.f, odd);
+      for (int i = 0; i < V; ++i) odd = fmaf(-kLog2e * x[i], 0.f, odd);
       uint32_t key[V];
       float m = 0.f, inv = 0.f;
       if (whole && __all_sync(kFull, odd == 0.f))
