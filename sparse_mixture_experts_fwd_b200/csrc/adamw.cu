@@ -32,8 +32,9 @@ constexpr int kRound = 2048;         // elements per block and round: 8 per thre
 constexpr int kLongChunk = 4 * kRound;
 constexpr int kLongChunk8 = 8 * kQBlock, kShortChunk8 = kQBlock;
 constexpr int kMaxTensors = 4096;
-constexpr int kSmallBatch = 32;      // tensors in the small launch parameter block
-constexpr int kLargeBatch = 384;     // and in the large one (27 KB of the 32 KB limit)
+// Tensors in a launch's parameter block: the large one is 26 KB of the 32 KB limit, and
+// a launch copies all of it.
+constexpr int kSmallBatch = 24, kMiddleBatch = 128, kLargeBatch = 384;
 // An |m| maximum below this stores the block's m as zeros: its scale's
 // reciprocal would leave fp32's range.
 constexpr float kTiny = 1e-30f;
@@ -52,7 +53,8 @@ struct AdamTensor {
 struct AdamHyper {
   float b1, nb1, b2, nb2, eps;      // nb = 1 - b, rounded from the double
   float one;                        // 1 (see add)
-  double lr, wd, step;
+  float decay, rate, root;          // from the host's step and lr (see StepScalars)
+  double wd;                        // the rest for the device's own
   double beta1, beta2;
   double max_norm;
   const double* norm;               // nullable
@@ -193,29 +195,38 @@ MOE_DEV uint32_t to_e4m3x4(const float (&f)[4]) {
   return q;
 }
 
-// The step's scalars, the same in every block.  Formed in fp64: 1 - b^t loses
-// its leading digits for b near 1 and small t.
-MOE_DEV StepScalars step_scalars(const AdamHyper& h) {
-  StepScalars s;
-  double t = h.step, lr = h.lr;
-  bool ok = true;
-  if (h.step_lr) {
-    t = h.step_lr[0];
-    lr = h.step_lr[1];
-    ok = t >= 1.0 && isfinite(t) && isfinite(lr);
+struct Rates {
+  float decay, rate, root;
+};
+// In fp64: 1 - b^t loses its leading digits for b near 1 and small t.
+__host__ __device__ inline Rates step_rates(double t, double lr, double wd, double beta1, double beta2) {
+  return Rates{static_cast<float>(1.0 - lr * wd), static_cast<float>(lr / (1.0 - pow(beta1, t))),
+               static_cast<float>(1.0 / sqrt(1.0 - pow(beta2, t)))};
+}
+
+// The step's scalars, the same in every block: the host's, unless the norm or the
+// step come from the device.  Every thread of the block calls it.
+MOE_DEV StepScalars step_scalars(const AdamHyper& h, StepScalars* shared) {
+  if (!h.norm && !h.step_lr) return StepScalars{1.0f, h.decay, h.rate, h.root, 0};
+  if (threadIdx.x == 0) {
+    StepScalars s{1.0f, h.decay, h.rate, h.root, 0};
+    if (h.step_lr) {
+      const double t = h.step_lr[0], lr = h.step_lr[1];
+      if (!(t >= 1.0) || !isfinite(t) || !isfinite(lr)) s.skip = 1;
+      const Rates r = step_rates(t, lr, h.wd, h.beta1, h.beta2);
+      s.decay = r.decay;
+      s.rate = r.rate;
+      s.root = r.root;
+    }
+    if (h.norm) {
+      const double n = *h.norm;
+      if (!isfinite(n)) s.skip = 1;
+      if (n > h.max_norm) s.clip = static_cast<float>(h.max_norm / n);
+    }
+    *shared = s;
   }
-  double clip = 1.0;
-  if (h.norm) {
-    const double n = *h.norm;
-    ok = ok && isfinite(n);
-    if (n > h.max_norm) clip = h.max_norm / n;
-  }
-  s.clip = static_cast<float>(clip);
-  s.decay = static_cast<float>(1.0 - lr * h.wd);
-  s.rate = static_cast<float>(lr / (1.0 - pow(h.beta1, t)));
-  s.root = static_cast<float>(1.0 / sqrt(1.0 - pow(h.beta2, t)));
-  s.skip = !ok;
-  return s;
+  __syncthreads();
+  return *shared;
 }
 
 // tensor of chunk c (last i with first[i] <= c)
@@ -238,9 +249,7 @@ adamw_kernel(const __grid_constant__ AdamBatch<N> b, const AdamHyper h) {
   __shared__ StepScalars s_step;
   dev::pdl_trigger();
   dev::pdl_wait();
-  if (threadIdx.x == 0) s_step = step_scalars(h);
-  __syncthreads();
-  const StepScalars s = s_step;
+  const StepScalars s = step_scalars(h, &s_step);
   if (s.skip) {
     if (blockIdx.x == 0 && threadIdx.x == 0 && h.status) atomicOr(h.status, MOE_STATUS_NONFINITE);
     return;
@@ -442,9 +451,7 @@ adamw8_kernel(const __grid_constant__ AdamBatch<N> b, const AdamHyper h) {
   __shared__ StepScalars s_step;
   dev::pdl_trigger();
   dev::pdl_wait();
-  if (threadIdx.x == 0) s_step = step_scalars(h);
-  __syncthreads();
-  const StepScalars s = s_step;
+  const StepScalars s = step_scalars(h, &s_step);
   if (s.skip) {
     if (blockIdx.x == 0 && threadIdx.x == 0 && h.status) atomicOr(h.status, MOE_STATUS_NONFINITE);
     return;
@@ -716,9 +723,14 @@ extern "C" int32_t moe_adamw_step(const moe_adamw_config* cfg, int32_t n, const 
   h.nb2 = static_cast<float>(1.0 - cfg->beta2);
   h.eps = static_cast<float>(cfg->eps);
   h.one = 1.0f;
-  h.lr = cfg->lr;
+  if (!step_lr) {
+    const Rates r = step_rates(static_cast<double>(cfg->step), cfg->lr, cfg->weight_decay,
+                               cfg->beta1, cfg->beta2);
+    h.decay = r.decay;
+    h.rate = r.rate;
+    h.root = r.root;
+  }
   h.wd = cfg->weight_decay;
-  h.step = static_cast<double>(cfg->step);
   h.beta1 = cfg->beta1;
   h.beta2 = cfg->beta2;
   h.max_norm = cfg->max_norm;
@@ -727,5 +739,6 @@ extern "C" int32_t moe_adamw_step(const moe_adamw_config* cfg, int32_t n, const 
   h.status = status;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   if (n <= kSmallBatch) return run_batches<kSmallBatch>(*cfg, n, l, h, s);
+  if (n <= kMiddleBatch) return run_batches<kMiddleBatch>(*cfg, n, l, h, s);
   return run_batches<kLargeBatch>(*cfg, n, l, h, s);
 }

@@ -137,7 +137,7 @@ def test_step_on_many_lengths(moe, bits, grad_dtype):
 
 
 @pytest.mark.parametrize("bits", [32, 8])
-@pytest.mark.parametrize("n", [1, 32, 33, 384, 385, 900])
+@pytest.mark.parametrize("n", [1, 24, 25, 32, 33, 128, 129, 384, 385, 900])
 def test_tensor_counts(moe, bits, n):
     before = make([(37 * i) % 700 for i in range(n)], bits, torch.float32, seed=n)
     D, ts, raws = on_device(moe, before, bits)
