@@ -170,8 +170,8 @@ const char* moe_error_string(int32_t code);
 const char* moe_last_error(void);
 
 /* 1 if this library was built with bounds checks (MOE_CHECK_BOUNDS: the file
- * libmoe_b200_checked.so), else 0.  In that build moe_dispatch and
- * moe_combine check every expert index and slot they are given against E and
+ * libmoe_b200_checked.so), else 0.  In that build moe_dispatch,
+ * moe_combine and their backward passes check every expert index and slot they are given against E and
  * C before they touch a row, skip a choice that is out of range and report
  * it as MOE_STATUS_BAD_INDEX; the expert-parallel calls always check their
  * rows (MOE_STATUS_BAD_COUNTS).  A debugging aid for callers that build the

@@ -264,7 +264,22 @@ def topk_assign(cfg, logits=None, domain_id=None, out=None, workspace=None, stat
     return o
 
 
+def _check_choices(cfg, expert_idx, slot, kept, gate=None):
+    """More than two choices: the arrays' types and shapes are settled, as in ``assign``."""
+    shape = (cfg.T, cfg.k)
+    _arg(expert_idx, "expert_idx", torch.int32, shape)
+    _arg(slot, "slot", torch.int32, shape)
+    _arg(kept, "kept", torch.uint8, shape)
+    if gate is not None:
+        _arg(gate, "gate", torch.float32, shape)
+
+
 def dispatch(cfg, x, expert_idx, slot, kept, xe=None, status=None, stream=None):
+    if cfg.k > 2:
+        _check_choices(cfg, expert_idx, slot, kept)
+        _arg(x, "x", _act_dtype(cfg), (cfg.T, cfg.d_model))
+        if xe is not None:
+            _arg_rows(xe, "xe", _act_dtype(cfg), (cfg.E, cfg.capacity, cfg.d_model))
     if xe is None:
         xe = torch.empty(cfg.E, cfg.capacity, cfg.d_model, dtype=x.dtype, device=x.device)
     _check(lib.moe_dispatch(ctypes.byref(cfg), _ptr(x, "x"), _ptr(expert_idx, "expert_idx"),
@@ -290,9 +305,9 @@ def _arg(t, name, dtype, shape):
 def _empty(shape, dtype, device, stream):
     """A new output, owned by the stream the call runs on."""
     if stream is None:
-        return torch.empty(shape, dtype=dtype, device=device)
+        return torch.empty(*shape, dtype=dtype, device=device)
     with torch.cuda.stream(stream):
-        return torch.empty(shape, dtype=dtype, device=device)
+        return torch.empty(*shape, dtype=dtype, device=device)
 
 
 def _arg_rows(t, name, dtype, rows):
@@ -360,8 +375,9 @@ def assign(cfg, expert_idx, out=None, status=None, stream=None):
     if not o:  # one allocation for the int32 outputs (five cost 12 us), pointers by offset
         n = T * k
         ints = _empty((n + E * C + 2 * E + 1,), torch.int32, expert_idx.device, stream)
+        # ("unsafe" for autograd only: the parts are no views of one another to it)
         slot, o["tok_of_row"], o["arrivals"], o["kept_cnt"], o["n_dropped"] = \
-            ints.split_with_sizes((n, E * C, E, E, 1))
+            torch.unsafe_split_with_sizes(ints, (n, E * C, E, E, 1))
         o["slot"] = slot.view(T, k)
         o["kept"] = _empty((T, k), torch.uint8, expert_idx.device, stream)
         at = ints.data_ptr()
@@ -452,6 +468,11 @@ def expert_ffn(cfg, xe, W1, W2, kept_cnt, H=None, ye=None, workspace=None, statu
 
 
 def combine(cfg, ye, expert_idx, gate, slot, kept, y=None, status=None, stream=None):
+    if cfg.k > 2:
+        _check_choices(cfg, expert_idx, slot, kept, gate)
+        _arg_rows(ye, "ye", _act_dtype(cfg), (cfg.E, cfg.capacity, cfg.d_model))
+        if y is not None:
+            _arg(y, "y", _act_dtype(cfg), (cfg.T, cfg.d_model))
     if y is None:
         y = torch.empty(cfg.T, cfg.d_model, dtype=ye.dtype, device=ye.device)
     _check(lib.moe_combine(ctypes.byref(cfg), _ptr(ye, "ye"), _ptr(expert_idx, "expert_idx"),

@@ -15,6 +15,7 @@
 #include <algorithm>
 #include <cfloat>
 #include <cmath>
+#include <new>
 #include <type_traits>
 #include <vector>
 
@@ -675,6 +676,11 @@ extern "C" int32_t moe_adamw_check(const moe_adamw_config* cfg, int32_t n, const
     bool written;
   };
   std::vector<Range> r;
+  try {
+    r.reserve(7 * static_cast<size_t>(n));
+  } catch (const std::bad_alloc&) {
+    return bad_arg("no host memory for the check");
+  }
   const bool bits8 = cfg->state_bits == 8;
   const int64_t es = bits8 ? 1 : 4;
   auto add = [&](const void* q, int64_t bytes, bool written) {

@@ -165,6 +165,23 @@ def test_route_border_hidden_behind_equal_ones(moe):
     check_route(moe, x, k, b, score="softmax")
 
 
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+def test_route_every_token_open(moe, score):
+    """More tokens that only fp64 can order than a block's list takes (every one of 400000)."""
+    g = torch.Generator().manual_seed(3)
+    E, distinct, T = 48, 40, 400_000
+    x = torch.full((distinct, E), 0.5).view(torch.int32)
+    x = (x + torch.stack([torch.randperm(E, generator=g) for _ in range(distinct)]).int()).view(torch.float32)
+    b = torch.full((E,), 0.25)
+    ri, rw = ref.route(x, 3, score=score, bias=b)
+    many = x.cuda().repeat(T // distinct, 1)
+    cfg = moe.make_route_config(T, E, 3, score=score)
+    idx, gate = moe.route(cfg, many, b.cuda())
+    assert torch.equal(idx, ri.cuda().repeat(T // distinct, 1))
+    err = (gate.double() - rw.cuda().repeat(T // distinct, 1)).abs()
+    assert float((err / rw.cuda().repeat(T // distinct, 1)).max()) <= 128 * U
+
+
 @pytest.mark.parametrize("dtype", DTYPES, ids=["f32", "bf16"])
 @pytest.mark.parametrize("score", ["softmax", "sigmoid"])
 def test_route_masks(moe, score, dtype):
@@ -456,6 +473,95 @@ def test_row_exchange(moe, case, dtype):
     _, mag = ref.combine_backward(x.abs(), rows.abs(), idx, gate, slot, kept)
     assert bool(((dgate[:T].cpu().double() - rdg).abs() <= (d / 32 + 16) * U * mag).all())
     assert bool((dgate[T] == -7).all())
+
+
+def test_row_exchange_refusals(moe):
+    case = (37, 16, 8, 20, 128)
+    T, E, k, C, d = case
+    idx, slot, kept, x, rows, gate = (t.cuda() for t in exchange(case, torch.bfloat16))
+    cfg = moe.make_config(T, d, 64, E, k, C)
+    with pytest.raises(ValueError, match="expert_idx"):
+        moe.dispatch(cfg, x, idx[:, :2].contiguous(), slot, kept)
+    with pytest.raises(ValueError, match="xe"):
+        moe.dispatch(cfg, x, idx, slot, kept, xe=rows[:, :-1].contiguous())
+    with pytest.raises(TypeError, match="kept"):
+        moe.combine(cfg, rows, idx, gate, slot, kept.int())
+    with pytest.raises(ValueError, match="ye"):
+        moe.combine(cfg, rows[:-1], idx, gate, slot, kept)
+    with pytest.raises(TypeError, match="dy"):
+        moe.combine_backward(cfg, x.float(), rows, idx, gate, slot, kept)
+    with pytest.raises(ValueError, match="dx"):
+        moe.dispatch_backward(cfg, rows, idx, slot, kept, dx=x[:-1])
+    with pytest.raises(moe.MoEError, match="k must be 1..16"):
+        moe.assign(moe.make_config(4, 64, 64, 32, 17, 2),
+                   torch.zeros(4, 17, dtype=torch.int32, device="cuda"))
+    with pytest.raises(moe.MoEError, match="k must be 1 or 2"):
+        moe.expert_ffn(cfg, rows, rows, rows, torch.zeros(E, dtype=torch.int32, device="cuda"),
+                       workspace=torch.zeros(4096, dtype=torch.uint8, device="cuda"))
+
+
+CHECKED = """
+import sys
+sys.path.insert(0, ROOT)
+sys.path.insert(0, ROOT + "/tests")
+import torch
+import sparse_mixture_experts_fwd_b200 as moe
+if moe.lib.moe_bounds_checked() != 1:
+    sys.exit(3)
+import routed_ref as ref
+T, E, k, C, d = 50, 12, 5, 30, 64
+g = torch.Generator().manual_seed(2)
+idx = torch.stack([torch.randperm(E, generator=g)[:k] for _ in range(T)]).int()
+a = ref.assign(idx, E, C)
+slot, kept = a["slot"].clone(), a["kept"].clone()
+good = kept.clone()
+bad = idx.clone()
+for t, j, e, s in ((1, 0, E, 0), (7, 2, -1, 1), (9, 4, 3, C), (20, 1, 4, -1)):
+    bad[t, j], slot[t, j] = e, s
+    kept[t, j], good[t, j] = 1, 0
+cfg = moe.make_config(T, d, 64, E, k, C, dtype=torch.float32)
+x = torch.randn(T, d, generator=g)
+rows = torch.randn(E, C, d, generator=g)
+gate = torch.rand(T, k, generator=g)
+st = torch.zeros(1, dtype=torch.int32, device="cuda")
+dev = [v.cuda() for v in (bad, slot, kept)]
+def reported():
+    torch.cuda.synchronize()
+    seen = int(st.item())
+    st.zero_()
+    return seen == moe.STATUS_BAD_INDEX
+big = torch.full((E * C + 8, d), -7.0, device="cuda")
+moe.dispatch(cfg, x.cuda(), *dev, xe=big[4:-4].view(E, C, d), status=st)
+assert reported()
+t, j, r = ref.rows_of(idx, slot, good, C)
+want = torch.full((E * C + 8, d), -7.0)
+want[4 + r] = x[t]
+assert torch.equal(big.cpu(), want)
+y = moe.combine(cfg, rows.cuda(), dev[0], gate.cuda(), dev[1], dev[2], status=st)
+assert reported()
+assert (y.cpu().double() - ref.gather(rows, idx, slot, good, gate)).abs().max() < 1e-5
+dx = moe.dispatch_backward(cfg, rows.cuda(), *dev, status=st)
+assert reported()
+assert (dx.cpu().double() - ref.gather(rows, idx, slot, good)).abs().max() < 1e-5
+dye, dg = moe.combine_backward(cfg, x.cuda(), rows.cuda(), dev[0], gate.cuda(), dev[1], dev[2], status=st)
+assert reported()
+rdye, rdg = ref.combine_backward(x, rows, idx, gate, slot, good)
+assert (dye.cpu().double() - rdye).abs().max() < 1e-5
+assert (dg.cpu().double() - rdg).abs().max() < 1e-4
+print("CHECKED_OK")
+"""
+
+
+def test_bounds_checked_build_skips_bad_choices(cuda_device):
+    """libmoe_b200_checked.so, in a process of its own that stops unless that build is loaded:
+    planted indices and slots outside the buffer are tested before a row is touched."""
+    import os
+    import subprocess
+    import sys
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", f"ROOT = {root!r}\n" + CHECKED], capture_output=True,
+                       text=True, timeout=300, env={**os.environ, "MOE_B200_CHECK_BOUNDS": "1"})
+    assert r.returncode == 0 and "CHECKED_OK" in r.stdout, r.stdout + r.stderr
 
 
 def test_combine_backward_in_place(moe):
