@@ -155,8 +155,12 @@ __global__ void __launch_bounds__(kThreads) scatter_kernel(const ChoiceParams p)
 // y or dx: the kept rows (times the gate), summed in choice order in fp32 and
 // rounded once.  Up to 8 rows are in flight: 16 would leave room for one block
 // an SM (65536 tokens x 16 rows of 256 bytes: 175 us then, 0.25 of the copy rate).
+// Bound by the bytes in flight, so for 8 rows 64 registers and four blocks an SM
+// (8191 tokens, rows of 5 KB: 59.2 us, 64.6 with the compiler's 70 registers and
+// three blocks) and for fewer rows 48 and five (16384 tokens, 4 rows of 2 KB: 30.9 us,
+// 42.1 with as many registers as the unrolled loads would take).
 template <int K, class V, int LANES>
-__global__ void __launch_bounds__(kThreads) gather_kernel(const ChoiceParams p) {
+__global__ void __launch_bounds__(kThreads, K == 16 ? 3 : K == 8 ? 4 : 5) gather_kernel(const ChoiceParams p) {
   dev::pdl_trigger();
   dev::pdl_wait();
   constexpr int N = V::kN;
@@ -194,7 +198,7 @@ __global__ void __launch_bounds__(kThreads) gather_kernel(const ChoiceParams p) 
         row[j] = __shfl_sync(0xffffffffu, mine.row, j);
         g[j] = __shfl_sync(0xffffffffu, mine.gate, j);
       }
-#pragma unroll(K >= 8 ? 1 : 8 / K)
+#pragma unroll(K >= 8 ? 1 : K >= 4 ? 2 : 4)
       for (int v = w.member; v < p.row_vec; v += w.team) {
 #pragma unroll
         for (int i = 0; i < N; ++i) acc[i] = 0.f;
@@ -272,12 +276,14 @@ __global__ void __launch_bounds__(kThreads) combine_backward_kernel(const Choice
     for (int j = 0; j < K; ++j) dot[j] = 0.f;
     const bool there = w.t < p.T;
     const uint4* src = p.tok_in + w.t * p.row_vec;
-    // choices b .. b + B - 1 of vector v
-    auto work = [&](const int64_t* row, const float* g, float* sums, const float (&dy)[N], int v) {
-      uint4 r[B];
+    // choices b .. b + B - 1: their rows' vector v, then what becomes of it
+    auto fetch = [&](const int64_t* row, uint4 (&r)[B], int v) {
 #pragma unroll
       for (int j = 0; j < B; ++j)
         if (row[j] >= 0) r[j] = p.row_in[row[j] + v];  // dye may be ye
+    };
+    auto work = [&](const int64_t* row, const float* g, float* sums, const uint4 (&r)[B],
+                    const float (&dy)[N], int v) {
 #pragma unroll
       for (int j = 0; j < B; ++j) {
         if (row[j] >= 0) {
@@ -301,11 +307,33 @@ __global__ void __launch_bounds__(kThreads) combine_backward_kernel(const Choice
         g[j] = __shfl_sync(0xffffffffu, mine.gate, j);
       }
       if (there) {
-        for (int v = w.member; v < p.row_vec; v += w.team) {
-          float dy[N];
-          V::unpack(__ldg(src + v), dy);
+        // up to 8 rows' vectors are loaded before any is stored: the compiler may not
+        // move loads over the stores by itself
+        constexpr int U = K >= 8 ? 1 : K >= 4 ? 2 : 4;
+        for (int v0 = w.member; v0 < p.row_vec; v0 += U * w.team) {
+          uint4 dv[U], r[U][B];
 #pragma unroll
-          for (int b = 0; b < K; b += B) work(row + b, g + b, dot + b, dy, v);
+          for (int u = 0; u < U; ++u) {
+            const int v = v0 + u * w.team;
+            if (v < p.row_vec) {
+              dv[u] = __ldg(src + v);
+              fetch(row, r[u], v);
+            }
+          }
+#pragma unroll
+          for (int u = 0; u < U; ++u) {
+            const int v = v0 + u * w.team;
+            if (v < p.row_vec) {
+              float dy[N];
+              V::unpack(dv[u], dy);
+              work(row, g, dot, r[u], dy, v);
+#pragma unroll
+              for (int b = B; b < K; b += B) {  // (K = 16: U is 1)
+                fetch(row + b, r[u], v);
+                work(row + b, g + b, dot + b, r[u], dy, v);
+              }
+            }
+          }
         }
       }
     } else {  // rows of at most LANES vectors: one each
@@ -321,7 +349,11 @@ __global__ void __launch_bounds__(kThreads) combine_backward_kernel(const Choice
           row[j] = __shfl_sync(0xffffffffu, mine.row, w.first + b + j);
           g[j] = __shfl_sync(0xffffffffu, mine.gate, w.first + b + j);
         }
-        if (on) work(row, g, dot + b, dy, w.member);
+        if (on) {
+          uint4 r[B];
+          fetch(row, r, w.member);
+          work(row, g, dot + b, r, dy, w.member);
+        }
       }
     }
     const float sum = reduce_many<K, LANES>(dot);
