@@ -264,22 +264,23 @@ def topk_assign(cfg, logits=None, domain_id=None, out=None, workspace=None, stat
     return o
 
 
-def _check_choices(cfg, expert_idx, slot, kept, gate=None):
-    """More than two choices: the arrays' types and shapes are settled, as in ``assign``."""
+def _choice_args(cfg, expert_idx, slot, kept):
+    """Pointers of the per-choice arrays [T, k]."""
     shape = (cfg.T, cfg.k)
-    _arg(expert_idx, "expert_idx", torch.int32, shape)
-    _arg(slot, "slot", torch.int32, shape)
-    _arg(kept, "kept", torch.uint8, shape)
-    if gate is not None:
-        _arg(gate, "gate", torch.float32, shape)
+    return (_arg(expert_idx, "expert_idx", torch.int32, shape),
+            _arg(slot, "slot", torch.int32, shape), _arg(kept, "kept", torch.uint8, shape))
 
 
 def dispatch(cfg, x, expert_idx, slot, kept, xe=None, status=None, stream=None):
-    if cfg.k > 2:
-        _check_choices(cfg, expert_idx, slot, kept)
-        _arg(x, "x", _act_dtype(cfg), (cfg.T, cfg.d_model))
-        if xe is not None:
-            _arg_rows(xe, "xe", _act_dtype(cfg), (cfg.E, cfg.capacity, cfg.d_model))
+    if cfg.k > 2:  # the arrays' types and shapes are settled, as in ``assign``
+        act, rows = _act_dtype(cfg), (cfg.E, cfg.capacity, cfg.d_model)
+        if xe is None:
+            xe = _empty(rows, act, x.device, stream)
+        _check(lib.moe_dispatch(ctypes.byref(cfg), _arg(x, "x", act, (cfg.T, cfg.d_model)),
+                                *_choice_args(cfg, expert_idx, slot, kept),
+                                _arg_rows(xe, "xe", act, rows), _status(status),
+                                _stream(stream)), "moe_dispatch")
+        return xe
     if xe is None:
         xe = torch.empty(cfg.E, cfg.capacity, cfg.d_model, dtype=x.dtype, device=x.device)
     _check(lib.moe_dispatch(ctypes.byref(cfg), _ptr(x, "x"), _ptr(expert_idx, "expert_idx"),
@@ -401,15 +402,13 @@ def assign(cfg, expert_idx, out=None, status=None, stream=None):
 
 def dispatch_backward(cfg, dxe, expert_idx, slot, kept, dx=None, status=None, stream=None):
     """Gradient of ``dispatch``: dx [T, d] sums the kept choices' rows of dxe [E, C, d]."""
-    T, k, act = cfg.T, cfg.k, _act_dtype(cfg)
+    T, act = cfg.T, _act_dtype(cfg)
     if dx is None:
         dx = _empty((T, cfg.d_model), act, dxe.device, stream)
     _check(lib.moe_dispatch_backward(
         ctypes.byref(cfg), _arg_rows(dxe, "dxe", act, (cfg.E, cfg.capacity, cfg.d_model)),
-        _arg(expert_idx, "expert_idx", torch.int32, (T, k)),
-        _arg(slot, "slot", torch.int32, (T, k)), _arg(kept, "kept", torch.uint8, (T, k)),
-        _arg(dx, "dx", act, (T, cfg.d_model)), _status(status), _stream(stream)),
-        "moe_dispatch_backward")
+        *_choice_args(cfg, expert_idx, slot, kept), _arg(dx, "dx", act, (T, cfg.d_model)),
+        _status(status), _stream(stream)), "moe_dispatch_backward")
     return dx
 
 
@@ -425,11 +424,10 @@ def combine_backward(cfg, dy, ye, expert_idx, gate, slot, kept, dye=None, dgate=
             dye.zero_()
     if dgate is None:
         dgate = _empty((T, k), torch.float32, ye.device, stream)
+    ep, sp, kp = _choice_args(cfg, expert_idx, slot, kept)
     _check(lib.moe_combine_backward(
-        ctypes.byref(cfg), _arg(dy, "dy", act, (T, cfg.d_model)), _arg_rows(ye, "ye", act, rows),
-        _arg(expert_idx, "expert_idx", torch.int32, (T, k)),
-        _arg(gate, "gate", torch.float32, (T, k)), _arg(slot, "slot", torch.int32, (T, k)),
-        _arg(kept, "kept", torch.uint8, (T, k)), _arg_rows(dye, "dye", act, rows),
+        ctypes.byref(cfg), _arg(dy, "dy", act, (T, cfg.d_model)), _arg_rows(ye, "ye", act, rows), ep,
+        _arg(gate, "gate", torch.float32, (T, k)), sp, kp, _arg_rows(dye, "dye", act, rows),
         _arg(dgate, "dgate", torch.float32, (T, k)), _status(status), _stream(stream)),
         "moe_combine_backward")
     return dye, dgate
@@ -469,10 +467,16 @@ def expert_ffn(cfg, xe, W1, W2, kept_cnt, H=None, ye=None, workspace=None, statu
 
 def combine(cfg, ye, expert_idx, gate, slot, kept, y=None, status=None, stream=None):
     if cfg.k > 2:
-        _check_choices(cfg, expert_idx, slot, kept, gate)
-        _arg_rows(ye, "ye", _act_dtype(cfg), (cfg.E, cfg.capacity, cfg.d_model))
-        if y is not None:
-            _arg(y, "y", _act_dtype(cfg), (cfg.T, cfg.d_model))
+        act = _act_dtype(cfg)
+        if y is None:
+            y = _empty((cfg.T, cfg.d_model), act, ye.device, stream)
+        ep, sp, kp = _choice_args(cfg, expert_idx, slot, kept)
+        _check(lib.moe_combine(
+            ctypes.byref(cfg), _arg_rows(ye, "ye", act, (cfg.E, cfg.capacity, cfg.d_model)), ep,
+            _arg(gate, "gate", torch.float32, (cfg.T, cfg.k)), sp, kp,
+            _arg(y, "y", act, (cfg.T, cfg.d_model)), _status(status), _stream(stream)),
+            "moe_combine")
+        return y
     if y is None:
         y = torch.empty(cfg.T, cfg.d_model, dtype=ye.dtype, device=ye.device)
     _check(lib.moe_combine(ctypes.byref(cfg), _ptr(ye, "ye"), _ptr(expert_idx, "expert_idx"),

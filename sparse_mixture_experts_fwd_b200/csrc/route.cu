@@ -341,9 +341,10 @@ __global__ void __launch_bounds__(kAssignThreads, 1) assign_kernel(const AssignA
 //                  totals are written;
 //   assign_wide:   slots from the block's prefix, the counts of its earlier warps and
 //                  the rank within the warp, as in assign_kernel.
-constexpr int kWideChunk = 2 * kAssignThreads;  // 2 rounds of 32 a warp
-constexpr int kWideRounds = 3;                  // the last block may take 255 more
-constexpr int64_t kWideFrom = 40 * kWideChunk;  // choices from which it is taken
+constexpr int kWideThreads = 512;
+constexpr int kWideChunk = 4 * kWideThreads;  // 4 rounds of 32 a warp
+constexpr int kWideRounds = 5;                // the last block may take 255 more
+constexpr int64_t kWideFrom = 65536;          // choices from which it is taken
 constexpr int64_t kOneUpTo = kAssignThreads;  // choices that one block takes
 constexpr int64_t kOneRows = 1 << 16;         // and the rows whose map it writes
 
@@ -366,10 +367,10 @@ __device__ __forceinline__ int wide_count(const WideArgs& p, int b) {
   return b + 1 < p.blocks ? kWideChunk : static_cast<int>(p.n_assign - wide_first(b));
 }
 
-__global__ void __launch_bounds__(kAssignThreads) assign_count_kernel(const WideArgs p) {
+__global__ void __launch_bounds__(kWideThreads) assign_count_kernel(const WideArgs p) {
   __shared__ int s_cnt[256];
   dev::pdl_trigger();
-  if (threadIdx.x < 256) s_cnt[threadIdx.x] = 0;
+  for (int i = threadIdx.x; i < 256; i += kWideThreads) s_cnt[i] = 0;
   dev::pdl_wait();
   __syncthreads();
   const int b = blockIdx.x, n = wide_count(p, b);
@@ -377,14 +378,14 @@ __global__ void __launch_bounds__(kAssignThreads) assign_count_kernel(const Wide
   int e[kWideRounds];
 #pragma unroll
   for (int r = 0; r < kWideRounds; ++r) {
-    const int i = r * kAssignThreads + threadIdx.x;
+    const int i = r * kWideThreads + threadIdx.x;
     e[r] = i < n ? __ldg(idx + i) : -1;
   }
 #pragma unroll
   for (int r = 0; r < kWideRounds; ++r)
     if (e[r] >= 0 && e[r] < p.E) atomicAdd(&s_cnt[e[r]], 1);
   __syncthreads();
-  if (threadIdx.x < p.E) p.slot[wide_first(b) + threadIdx.x] = s_cnt[threadIdx.x];
+  for (int e_ = threadIdx.x; e_ < p.E; e_ += kWideThreads) p.slot[wide_first(b) + e_] = s_cnt[e_];
 }
 
 // 32 experts (lanes) per block; a warp takes a run of the blocks' counts
@@ -427,25 +428,26 @@ __global__ void __launch_bounds__(kAssignThreads) assign_scan_kernel(const WideA
 // ONE: a single block has the whole list, a round a warp, and writes the totals
 // itself.
 template <bool ONE>
-__global__ void __launch_bounds__(kAssignThreads, 1) assign_wide_kernel(const WideArgs p) {
+__global__ void __launch_bounds__(ONE ? kAssignThreads : kWideThreads) assign_wide_kernel(const WideArgs p) {
   constexpr int kRounds = ONE ? 1 : kWideRounds;
+  constexpr int kThreads = ONE ? kAssignThreads : kWideThreads, kWarps = kThreads / 32;
   extern __shared__ int s_mem[];
   const int E = p.E;
   const int Ep = E | 1;      // odd stride: a column (one expert, all warps) in 32 banks
-  int* s_cnt = s_mem;        // [32 warps][Ep]
-  int* s_base = s_cnt + 32 * Ep;  // [E] earlier blocks' choices; ONE: all choices
+  int* s_cnt = s_mem;        // [kWarps][Ep]
+  int* s_base = s_cnt + kWarps * Ep;  // [E] earlier blocks' choices; ONE: all choices
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const unsigned lower = (1u << lane) - 1u;
   dev::pdl_trigger();
-  for (int i = tid; i < 32 * Ep; i += kAssignThreads) s_cnt[i] = 0;
+  for (int i = tid; i < kWarps * Ep; i += kThreads) s_cnt[i] = 0;
   dev::pdl_wait();
   const int b = blockIdx.x;
   const int n = ONE ? static_cast<int>(p.n_assign) : wide_count(p, b);
   const int64_t first = ONE ? 0 : wide_first(b);
   if (!ONE)
-    for (int x = tid; x < E; x += kAssignThreads) s_base[x] = p.slot[first + x];
+    for (int x = tid; x < E; x += kThreads) s_base[x] = p.slot[first + x];
   // a warp's run of consecutive choices, in rounds of 32
-  const int per_warp = (n + 32 * 32 - 1) / (32 * 32) * 32;
+  const int per_warp = (n + kThreads - 1) / kThreads * 32;
   const int w0 = warp * per_warp, w1 = min(w0 + per_warp, n);
   int ev[kRounds], lv[kRounds];
 #pragma unroll
@@ -469,16 +471,15 @@ __global__ void __launch_bounds__(kAssignThreads, 1) assign_wide_kernel(const Wi
     }
   }
   __syncthreads();
-  for (int x = warp; x < E; x += kAssignThreads / 32) {  // exclusive prefix over the warps
-    const int c = s_cnt[lane * Ep + x];
-    int incl = c;
+  for (int x = tid; x < E; x += kThreads) {  // exclusive prefix over the warps
+    int sum = 0;
 #pragma unroll
-    for (int off = 1; off < 32; off <<= 1) {
-      const int o = __shfl_up_sync(0xffffffffu, incl, off);
-      if (lane >= off) incl += o;
+    for (int w = 0; w < kWarps; ++w) {
+      const int c = s_cnt[w * Ep + x];
+      s_cnt[w * Ep + x] = sum;
+      sum += c;
     }
-    s_cnt[lane * Ep + x] = incl - c;
-    if (ONE && lane == 31) s_base[x] = incl;
+    if (ONE) s_base[x] = sum;
   }
   __syncthreads();
 #pragma unroll
@@ -495,13 +496,13 @@ __global__ void __launch_bounds__(kAssignThreads, 1) assign_wide_kernel(const Wi
     }
   }
   if (ONE) {
-    for (int x = tid; x < E; x += kAssignThreads) {
+    for (int x = tid; x < E; x += kThreads) {
       p.arrivals[x] = s_base[x];
       p.kept_cnt[x] = min(s_base[x], p.C);
     }
   }
   // the free rows, an expert at a time per warp of the grid, and the dropped total
-  for (int x = b * 32 + warp; x < E; x += static_cast<int>(gridDim.x) * 32) {
+  for (int x = b * kWarps + warp; x < E; x += static_cast<int>(gridDim.x) * kWarps) {
     for (int r = (ONE ? min(s_base[x], p.C) : p.kept_cnt[x]) + lane; r < p.C; r += 32)
       p.tok_of_row[static_cast<int64_t>(x) * p.C + r] = -1;
   }
@@ -678,8 +679,8 @@ int32_t launch_assign(const moe_config& c, const int32_t* expert_idx, int32_t* s
 
 // moe_assign: one block for short lists, one cluster for longer ones, the whole GPU
 // for long ones.  Measured, one against the other (us): block / cluster 512 choices
-// 3.9 / 5.1, 4096 8.7 / 5.8; cluster / GPU 16 k 9.4 / 14.3, 131 k 17.4 / 13.9,
-// 524 k (256 experts) 76 / 17.4, 1 M 133 / 27.
+// 3.9 / 5.1, 4096 8.7 / 5.8; cluster / GPU 16 k 5.9 / 9.5, 65 k 10.4 / 9.9, 131 k
+// 17.4 / 10.9, 524 k (256 experts) 76 / 14.3, 1 M 133 / 22.
 int32_t launch_assign_choices(const moe_config& c, const int32_t* expert_idx, int32_t* slot,
                               uint8_t* kept, int32_t* tok_of_row, int32_t* arrivals,
                               int32_t* kept_cnt, int32_t* n_dropped, cudaStream_t s) {
@@ -699,19 +700,20 @@ int32_t launch_assign_choices(const moe_config& c, const int32_t* expert_idx, in
   p.arrivals = arrivals;
   p.kept_cnt = kept_cnt;
   p.n_dropped = n_dropped;
-  const size_t smem = (32 * static_cast<size_t>(c.E | 1) + c.E) * sizeof(int);
-  const dim3 block(kAssignThreads);
+  auto smem = [&](int threads) {
+    return (threads / 32 * static_cast<size_t>(c.E | 1) + c.E) * sizeof(int);
+  };
   if (one) {
-    launch_pdl(assign_wide_kernel<true>, dim3(1), block, smem, s, p);
+    launch_pdl(assign_wide_kernel<true>, dim3(1), dim3(kAssignThreads), smem(kAssignThreads), s, p);
     return check_launch("assign_wide_kernel");
   }
   p.blocks = static_cast<int>(p.n_assign / kWideChunk);
   // a last block needs room for its counts; fewer choices go to the one before
   if (p.n_assign - wide_first(p.blocks) >= 256) ++p.blocks;
-  const dim3 grid(static_cast<unsigned>(p.blocks));
+  const dim3 grid(static_cast<unsigned>(p.blocks)), block(kWideThreads);
   launch_pdl(assign_count_kernel, grid, block, 0, s, p);
-  launch_pdl(assign_scan_kernel, dim3((c.E + 31) / 32), block, 0, s, p);
-  launch_pdl(assign_wide_kernel<false>, grid, block, smem, s, p);
+  launch_pdl(assign_scan_kernel, dim3((c.E + 31) / 32), dim3(kAssignThreads), 0, s, p);
+  launch_pdl(assign_wide_kernel<false>, grid, block, smem(kWideThreads), s, p);
   return check_launch("assign_wide_kernel");
 }
 
