@@ -163,11 +163,14 @@ def _ptr(t, name):
     return t.data_ptr()
 
 
+_current_device, _current_stream = torch._C._cuda_getDevice, torch._C._cuda_getCurrentRawStream
+
+
 def _stream(stream=None) -> int:
     if stream is not None:
         return stream.cuda_stream
     # the handle alone: building torch's Stream object costs 3 us a call
-    return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
+    return _current_stream(_current_device())
 
 
 def capacity(T: int, E: int, capacity_factor: float) -> int:
@@ -291,9 +294,10 @@ def dispatch(cfg, x, expert_idx, slot, kept, xe=None, status=None, stream=None):
 
 def _arg(t, name, dtype, shape):
     """Device pointer of an argument whose dtype, shape and device are settled."""
-    if t.dtype is dtype and t.shape == shape and t.is_cuda and t.is_contiguous() and \
-            t.get_device() == torch._C._cuda_getDevice():
-        return t.data_ptr()
+    if t.dtype is dtype and t.shape == shape and t.is_contiguous():
+        dev = t.get_device()  # -1: a CPU tensor
+        if dev >= 0 and dev == _current_device():
+            return t.data_ptr()
     if t.dtype is not dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
     if t.shape != shape:
