@@ -174,12 +174,13 @@ __global__ void __launch_bounds__(kThreads, K == 16 ? 3 : K == 8 ? 4 : 5) gather
     next = choice_of(p, w.t + w.step, j0, &bad);
     uint4* dst = p.tok_out + w.t * p.row_vec;
     float acc[N];
-    // choices b .. b + B - 1 of vector v into acc
-    auto add = [&](const int64_t* row, const float* g, int v) {
-      uint4 r[B];
+    // choices b .. b + B - 1: their rows' vector v, then its part of the sum
+    auto fetch = [&](const int64_t* row, uint4 (&r)[B], int v) {
 #pragma unroll
       for (int j = 0; j < B; ++j)
         if (row[j] >= 0) r[j] = __ldg(p.row_in + row[j] + v);
+    };
+    auto add = [&](const int64_t* row, const float* g, const uint4 (&r)[B]) {
 #pragma unroll
       for (int j = 0; j < B; ++j) {
         if (row[j] >= 0) {
@@ -198,13 +199,27 @@ __global__ void __launch_bounds__(kThreads, K == 16 ? 3 : K == 8 ? 4 : 5) gather
         row[j] = __shfl_sync(0xffffffffu, mine.row, j);
         g[j] = __shfl_sync(0xffffffffu, mine.gate, j);
       }
-#pragma unroll(K >= 8 ? 1 : K >= 4 ? 2 : 4)
-      for (int v = w.member; v < p.row_vec; v += w.team) {
+      constexpr int U = K >= 8 ? 1 : K >= 4 ? 2 : 4;  // up to 8 vectors ahead of the sums
+      for (int v0 = w.member; v0 < p.row_vec; v0 += U * w.team) {
+        uint4 r[U][B];
 #pragma unroll
-        for (int i = 0; i < N; ++i) acc[i] = 0.f;
+        for (int u = 0; u < U; ++u)
+          if (v0 + u * w.team < p.row_vec) fetch(row, r[u], v0 + u * w.team);
 #pragma unroll
-        for (int b = 0; b < K; b += B) add(row + b, g + b, v);
-        dst[v] = V::pack(acc);
+        for (int u = 0; u < U; ++u) {
+          const int v = v0 + u * w.team;
+          if (v < p.row_vec) {
+#pragma unroll
+            for (int i = 0; i < N; ++i) acc[i] = 0.f;
+            add(row, g, r[u]);
+#pragma unroll
+            for (int b = B; b < K; b += B) {  // (K = 16: U is 1)
+              fetch(row + b, r[u], v);
+              add(row + b, g + b, r[u]);
+            }
+            dst[v] = V::pack(acc);
+          }
+        }
       }
     } else {  // rows of at most LANES vectors: one each
       const bool on = w.t < p.T && w.member < p.row_vec;
@@ -219,7 +234,11 @@ __global__ void __launch_bounds__(kThreads, K == 16 ? 3 : K == 8 ? 4 : 5) gather
           row[j] = __shfl_sync(0xffffffffu, mine.row, w.first + b + j);
           g[j] = __shfl_sync(0xffffffffu, mine.gate, w.first + b + j);
         }
-        if (on) add(row, g, w.member);
+        if (on) {
+          uint4 r[B];
+          fetch(row, r, w.member);
+          add(row, g, r);
+        }
       }
       if (on) dst[w.member] = V::pack(acc);
     }
