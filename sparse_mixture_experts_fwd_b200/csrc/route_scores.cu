@@ -285,9 +285,10 @@ MOE_DEV void sort_desc(uint32_t (&v)[N]) {
 }
 
 // A lane's sorted keys: the first in `head`, the others behind it in the lane's
-// column of shared memory (its own reads and writes only, so nothing waits).
-// Taking the first away is then one predicated load; shifting V registers costs V
-// instructions of the whole warp.
+// column of shared memory (its own reads and writes only, so nothing waits), and
+// zeros behind those.  Taking the first away is then one predicated load; shifting V
+// registers costs V instructions of the whole warp.
+constexpr int kZeroRows = kMaxChoices + 1;  // what k takes from an empty list may read
 template <int V>
 struct KeyList {
   uint32_t head;
@@ -297,12 +298,10 @@ struct KeyList {
 #pragma unroll
     for (int i = 1; i < V; ++i)
       asm volatile("st.shared.u32 [%0], %1;" ::"r"(column + 128u * (i - 1)), "r"(key[i]) : "memory");
-    asm volatile("st.shared.u32 [%0], %1;" ::"r"(column + 128u * (V - 1)), "r"(0u) : "memory");
     next = column;
   }
-  // the first key, if it is `top` (the warp's largest; 0: nothing is left), goes
-  MOE_DEV void take(uint32_t top) {
-    if (head == top && top != 0u) {
+  MOE_DEV void take(uint32_t top) {  // the first key, if it is `top` (the warp's largest), goes
+    if (head == top) {
       asm volatile("ld.shared.u32 %0, [%1];" : "=r"(head) : "r"(next) : "memory");
       next += 128u;
     }
@@ -393,10 +392,11 @@ MOE_DEV void check_inputs(const RouteParams& p, const L* h, bool has_bias, unsig
                           uint32_t mine, int rel, uint32_t last, KeyList<V> list, bool& close,
                           bool& edge) {
   const bool there = rel >= 0 && rel < p.k && mine != 0u;
+  const uint32_t after = __shfl_down_sync(kFull, mine, 1);
   const int e = there ? expert_of(mine) : 0;
   const float x = there ? to_float(h[e]) : 0.f, b = there && has_bias ? __ldg(p.bias + e) : 0.f;
   const float xa = __shfl_down_sync(kFull, x, 1), ba = __shfl_down_sync(kFull, b, 1);
-  close = close && !(x == xa && b == ba);
+  close = close && after != 0u && !(x == xa && b == ba);
   if (edge) {
     const int el = expert_of(last);
     const float xl = to_float(h[el]), bl = has_bias ? __ldg(p.bias + el) : 0.f;
@@ -502,9 +502,9 @@ MOE_DEV bool settle_groups(const RouteParams& p, const L* h, bool has_bias, unsi
 template <typename L, int V, int W, int MODE>
 __global__ void __launch_bounds__(kWarps * 32, blocks_per_sm(V))
 route_kernel(const __grid_constant__ RouteParams p) {
-  // per warp: the lanes' key lists, or route_exact's candidates
+  // per warp: the lanes' key lists, and after the loop route_exact's candidates
   __shared__ union {
-    uint32_t column[V][32];
+    uint32_t column[V - 1 + kZeroRows][32];
     unsigned long long candidate[256];
   } s_warp[kWarps];
   __shared__ int32_t s_open[kMaxOpen];
@@ -543,7 +543,8 @@ route_kernel(const __grid_constant__ RouteParams p) {
     }
     from += p.E;
   };
-  float ahead[V];  // the next token's logits; the first are on their way during the set-up
+  float ahead[V];  // the next token's logits: on their way during the set-up, and once a
+                   // token's are keys during its choice
   if (count > 0) load_row(ahead);
   float off[V];    // score modes: the bias's part of the key; NaN masks the expert
   float unit = 0.f;
@@ -579,6 +580,7 @@ route_kernel(const __grid_constant__ RouteParams p) {
   whole = __all_sync(kFull, whole);
 
   const uint32_t column = dev::smem_u32(&s_warp[warp].column[0][lane]);
+  for (int i = 0; i < kZeroRows; ++i) s_warp[warp].column[V - 1 + i][lane] = 0u;
   // in the weights' part lane slot * seg + j works for choice j of a batch's token `slot`
   const int my_slot = lane / p.seg, my_j = lane & (p.seg - 1);
 
@@ -588,21 +590,18 @@ route_kernel(const __grid_constant__ RouteParams p) {
     float my_m = 0.f, my_inv = 0.f;
     unsigned open = 0u;      // slots whose order fp32 could not tell
     for (int slot = 0; slot < in_batch; ++slot) {
-      float x[V];
-#pragma unroll
-      for (int i = 0; i < V; ++i) x[i] = ahead[i];
-      if (done + slot + 1 < count) load_row(ahead);
       // 0 unless a logit is masked, NaN or infinite (or above 2.3e38): the product
       // overflows for the lowest values too, and inf * 0 is NaN
       float odd = 0.f;
 #pragma unroll
-      for (int i = 0; i < V; ++i) odd = fmaf(-kLog2e * x[i], 0.f, odd);
+      for (int i = 0; i < V; ++i) odd = fmaf(-kLog2e * ahead[i], 0.f, odd);
       uint32_t key[V];
       float m = 0.f, inv = 0.f;
       if (whole && __all_sync(kFull, odd == 0.f))
-        make_keys<L, V, W, MODE, false>(p, x, off, unit, first + li * W, sums, key, m, inv, bad);
+        make_keys<L, V, W, MODE, false>(p, ahead, off, unit, first + li * W, sums, key, m, inv, bad);
       else
-        make_keys<L, V, W, MODE, true>(p, x, off, unit, first + li * W, sums, key, m, inv, bad);
+        make_keys<L, V, W, MODE, true>(p, ahead, off, unit, first + li * W, sums, key, m, inv, bad);
+      if (done + slot + 1 < count) load_row(ahead);
       sort_desc<V>(key);
 
       bool unsure = false;
@@ -627,7 +626,7 @@ route_kernel(const __grid_constant__ RouteParams p) {
         }
         bool out = g != 0u;
         // a group left out that may be as good as the last one that stays
-        const bool near_out = !kExactKey && out && (last >> 5) - (g >> 5) <= 2 * kNear;
+        const bool near_out = !kExactKey && out && last - g < (2 * kNear + 1) << 5;
         if (__any_sync(kFull, near_out || unsure)) {
           unsure = __any_sync(kFull, unsure);
           if constexpr (MODE != kBySoftmax && !kExactKey) {
@@ -653,8 +652,11 @@ route_kernel(const __grid_constant__ RouteParams p) {
       if constexpr (!kExactKey) {
         // neighbours in the order, and the last choice against what this lane has left
         const uint32_t after = __shfl_down_sync(kFull, mine, 1);
-        bool close = rel >= 0 && rel + 1 < p.k && after != 0u && (mine >> 9) - (after >> 9) <= kNear;
-        bool edge = list.head != 0u && (last >> 9) - (list.head >> 9) <= kNear;
+        // (whole keys: the experts' bits only widen it, and a 0 in place of a key is
+        // sorted out below)
+        bool close = static_cast<unsigned>(rel) < static_cast<unsigned>(p.k - 1) &&
+                     mine - after < (kNear + 1) << 9;
+        bool edge = last - list.head < (kNear + 1) << 9;
         if (__any_sync(kFull, close || edge)) {
           const L* h = rows + static_cast<int64_t>(done + slot) * p.E;
           check_inputs(p, h, has_bias, kNear, mine, rel, last, list, close, edge);
