@@ -293,12 +293,13 @@ template <int V>
 struct KeyList {
   uint32_t head;
   uint32_t next;  // shared-memory address
-  MOE_DEV void fill(const uint32_t (&key)[V], uint32_t column) {
-    head = key[0];
+  // out: none of the lane's keys may be chosen (its group is left out)
+  MOE_DEV void fill(const uint32_t (&key)[V], uint32_t column, bool out) {
+    head = out ? 0u : key[0];
 #pragma unroll
     for (int i = 1; i < V; ++i)
       asm volatile("st.shared.u32 [%0], %1;" ::"r"(column + 128u * (i - 1)), "r"(key[i]) : "memory");
-    next = column;
+    next = out ? column + 128u * (V - 1) : column;
   }
   MOE_DEV void take(uint32_t top) {  // the first key, if it is `top` (the warp's largest), goes
     if (head == top) {
@@ -604,7 +605,7 @@ route_kernel(const __grid_constant__ RouteParams p) {
       if (done + slot + 1 < count) load_row(ahead);
       sort_desc<V>(key);
 
-      bool unsure = false;
+      bool unsure = false, out = false;
       if (p.G > 1) {
         uint32_t a1 = key[0], a2 = V > 1 ? key[V > 1 ? 1 : 0] : 0u;
         for (int o = 1; o < p.lanes; o <<= 1) {
@@ -624,7 +625,7 @@ route_kernel(const __grid_constant__ RouteParams p) {
           last = __reduce_max_sync(kFull, g);
           if (g == last) g = 0u;
         }
-        bool out = g != 0u;
+        out = g != 0u;
         // a group left out that may be as good as the last one that stays
         const bool near_out = !kExactKey && out && last - g < (2 * kNear + 1) << 5;
         if (__any_sync(kFull, near_out || unsure)) {
@@ -636,11 +637,10 @@ route_kernel(const __grid_constant__ RouteParams p) {
             unsure = true;
           }
         }
-        if (out) key[0] = 0u;  // the list behind a 0 is never reached
       }
 
       KeyList<V> list;
-      list.fill(key, column);
+      list.fill(key, column, out);
       uint32_t last = 0u;
       const int rel = lane - slot * p.seg;
 #pragma unroll 4

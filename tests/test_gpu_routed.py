@@ -212,6 +212,26 @@ def test_route_masks(moe, score, dtype):
 
 
 @pytest.mark.parametrize("dtype", DTYPES, ids=["f32", "bf16"])
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+def test_route_groups_with_few_left(moe, score, dtype):
+    """The groups that stay hold fewer experts than k while those left out hold more: the rest of
+    the choices is -1, not an expert of a group that was left out."""
+    g = torch.Generator().manual_seed(21)
+    T, E, per = 60, 64, 8
+    x = torch.randn(T, E, generator=g)
+    left = torch.randint(0, 4, (T, E // per), generator=g)      # 0 to 3 of 8 left in each group
+    order = torch.rand(T, E // per, per, generator=g).argsort(2)
+    x = torch.where(order.view(T, E) < left.repeat_interleave(per, 1), x, -math.inf).to(dtype)
+    b = 0.1 * torch.randn(E, generator=g)
+    for bias in (None, b):
+        for gt in (1, 2):
+            for k, tg in ((8, 1), (16, 2), (16, 3), (5, 2)):
+                idx, _ = check_route(moe, x, k, bias, score=score, groups=8, top_groups=tg,
+                                     group_top=gt)
+                assert bool((idx == -1).any())
+
+
+@pytest.mark.parametrize("dtype", DTYPES, ids=["f32", "bf16"])
 def test_route_nan_and_inf_are_masked_and_reported(moe, dtype):
     g = torch.Generator().manual_seed(1)
     x = torch.randn(20, 24, generator=g).to(dtype)
