@@ -5,7 +5,10 @@
 //   combine             y[t, :] = sum over kept j of w_j ye[e_j, s_j, :]
 //   combine, backward   dye[e_j, s_j, :] = w_j dy[t, :],  dw_j = <dy[t], ye[e_j, s_j]>
 // A kept choice owns its expert row, so no two tokens touch the same one and
-// nothing is added atomically.
+// nothing is added atomically.  All of them are copies of rows by 16-byte vectors,
+// bound by HBM and the bytes in flight.  16384 tokens, 8 kept choices, rows of
+// 2 KB, 302 MB one way (46 us at the copy rate): dispatch 54 us, combine 49,
+// dispatch's gradient 49, combine's (570 MB, 87 us) 98.  5 tokens: 3.6 us.
 #include <algorithm>
 #include <type_traits>
 

@@ -294,8 +294,6 @@ def test_eight_bit_codes_are_the_formulas(moe):
                 code = torch.where(blocks > 0, code.clamp(min=2.0 ** -9), code)
             code = code.to(torch.float8_e4m3fn)
             assert torch.equal(q[name + "_scale"], scale.view(-1)), (name, step)
-            # the root is the rounded one but for one value in 2^18, and of those one in a
-            # million or so lies at a border
             differ = int((q[name].view(torch.uint8) != code.view(-1).view(torch.uint8)).sum())
             assert differ == 0, (name, step, differ)
             back = code.float() * scale
