@@ -13,10 +13,12 @@
 //
 // Bound by instruction issue: 65536 x 256 fp32 logits, 8 experts in 4 of 8 groups by
 // sigmoid scores with a bias, 39.9 us, about 470 warp instructions a token; the
-// logits' bytes alone would take 10.9.  4 tokens: 4.0 us.
+// logits' bytes alone would take 10.9.  4 tokens: 4.0 us.  Layers of few experts take
+// a thread per token (route_few_kernel).
 #include <cfloat>
 #include <climits>
 #include <cmath>
+#include <type_traits>
 
 #include "moe_internal.cuh"
 
@@ -25,6 +27,7 @@ namespace {
 
 constexpr unsigned kFull = 0xffffffffu;
 constexpr int kWarps = 8;  // warps per block, a token each
+constexpr int kFewThreads = 128;  // of route_few_kernel's blocks
 constexpr int kMaxOpen = 512;  // tokens a block lists for its fp64 pass
 constexpr int32_t kOpenMark = INT_MIN;  // in expert_idx until then: one that did not fit the list
 // A logit at or below bf16's lowest value masks its expert, as -inf does.
@@ -711,6 +714,159 @@ route_kernel(const __grid_constant__ RouteParams p) {
   if (__any_sync(kFull, bad) && lane == 0 && p.status) atomicOr(p.status, MOE_STATUS_BAD_LOGIT);
 }
 
+// Few experts (E <= EM <= 16) and many tokens: a thread per token, everything in its
+// registers.  The order is decided by the logits themselves or, with a bias or sums of
+// two scores, by scores in fp64 for all of them: with so few it costs less than
+// telling where fp32 would do.  launch_route_t says from how many tokens.
+template <typename L, int EM, bool BY_LOGIT>
+__global__ void __launch_bounds__(kFewThreads) route_few_kernel(const __grid_constant__ RouteParams p) {
+  using C = typename std::conditional<BY_LOGIT, float, double>::type;
+  constexpr C kNone = -INFINITY;
+  dev::pdl_trigger();
+  dev::pdl_wait();
+  bool bad = false;
+  const int64_t stride = static_cast<int64_t>(gridDim.x) * kFewThreads;
+  for (int64_t t = static_cast<int64_t>(blockIdx.x) * kFewThreads + threadIdx.x; t < p.T; t += stride) {
+    const L* h = static_cast<const L*>(p.logits) + t * p.E;
+    float x[EM];
+    if (p.E % 4 == 0) {
+#pragma unroll
+      for (int i = 0; i < EM; i += 4) {
+        if (i < p.E) load_logits<4>(h + i, x + i);
+        else x[i] = x[i + 1] = x[i + 2] = x[i + 3] = -INFINITY;
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < EM; ++i) x[i] = i < p.E ? to_float(h[i]) : -INFINITY;
+    }
+    float m = -INFINITY;
+#pragma unroll
+    for (int i = 0; i < EM; ++i) {
+      if (!counts(x[i])) {
+        if (!(x[i] < 0.f)) bad = true;  // NaN or +inf
+        x[i] = -INFINITY;
+      }
+      m = fmaxf(m, x[i]);
+    }
+    // what decides; an expert that cannot be chosen has kNone
+    C c[EM];
+    if constexpr (BY_LOGIT) {
+#pragma unroll
+      for (int i = 0; i < EM; ++i) c[i] = x[i];
+    } else {
+      double sum = 0.0;
+#pragma unroll
+      for (int i = 0; i < EM; ++i) {
+        const double z = static_cast<double>(x[i]);
+        c[i] = x[i] == -INFINITY ? 0.0 : p.sigmoid ? 1.0 / (1.0 + exp(-z)) : exp(z - m);
+        sum += c[i];
+      }
+#pragma unroll
+      for (int i = 0; i < EM; ++i) {
+        if (!p.sigmoid) c[i] /= sum;
+        bool can = x[i] > -INFINITY;
+        if (p.bias && i < p.E) {
+          const float b = __ldg(p.bias + i);
+          if (!(fabsf(b) < INFINITY)) {
+            if (!(b < 0.f)) bad = true;
+            can = false;
+          }
+          c[i] += static_cast<double>(b);
+        }
+        if (!can) c[i] = kNone;
+      }
+    }
+    unsigned allowed = (1u << EM) - 1u;
+    if (p.G > 1) {
+      C value[EM];
+#pragma unroll
+      for (int g = 0; g < EM; ++g) {
+        value[g] = kNone;
+        if (g < p.G) {
+          C b1 = kNone, b2 = kNone;
+#pragma unroll
+          for (int i = 0; i < EM; ++i) {
+            if (i >= g * p.gs && i < (g + 1) * p.gs) {
+              if (c[i] > b1) {
+                b2 = b1;
+                b1 = c[i];
+              } else if (c[i] > b2) {
+                b2 = c[i];
+              }
+            }
+          }
+          value[g] = p.group_top == 2 && b2 > kNone ? b1 + b2 : b1;
+        }
+      }
+      allowed = 0u;
+      for (int n = 0; n < p.top_groups; ++n) {
+        C best = kNone;
+        int bg = -1;
+#pragma unroll
+        for (int g = 0; g < EM; ++g)
+          if (value[g] > best) {
+            best = value[g];
+            bg = g;
+          }
+        if (bg < 0) break;
+        allowed |= ((1u << p.gs) - 1u) << (bg * p.gs);
+#pragma unroll
+        for (int g = 0; g < EM; ++g)
+          if (g == bg) value[g] = kNone;
+      }
+    }
+    unsigned long long order = 0ull;  // 4 bits a choice
+    int n = 0;
+    unsigned taken = 0u;
+    for (; n < p.k; ++n) {
+      C best = kNone;
+      int be = -1;
+#pragma unroll
+      for (int i = 0; i < EM; ++i)
+        if (((allowed & ~taken) >> i & 1u) && c[i] > best) {
+          best = c[i];
+          be = i;
+        }
+      if (be < 0) break;
+      order |= static_cast<unsigned long long>(be) << (4 * n);
+      taken |= 1u << be;
+    }
+    // weights of the chosen experts, as in choice_weight
+    float w[EM], sum = 0.f, ref = 0.f;
+    if (p.renorm) {
+      float mx = -INFINITY;
+#pragma unroll
+      for (int i = 0; i < EM; ++i)
+        if (taken >> i & 1u) mx = fmaxf(mx, x[i]);
+      ref = p.sigmoid ? fminf(mx, 0.f) : mx;
+    } else if (!p.sigmoid) {
+      ref = m;
+    }
+#pragma unroll
+    for (int i = 0; i < EM; ++i) {
+      w[i] = 0.f;
+      const bool chosen = taken >> i & 1u;
+      if (chosen || (!p.renorm && !p.sigmoid && x[i] > -INFINITY)) {
+        const bool up = p.sigmoid && x[i] >= 0.f;
+        w[i] = expf(up ? -x[i] : x[i] - ref);
+        if (p.sigmoid) w[i] = __fdividef(up ? 1.0f : w[i], 1.0f + (up ? w[i] : expf(x[i])));
+        sum += w[i];
+      }
+    }
+    const float f = p.renorm || !p.sigmoid ? (sum > 0.f ? __fdividef(1.0f, sum) : 0.f) : 1.0f;
+    for (int j = 0; j < p.k; ++j) {
+      const int e = j < n ? static_cast<int>(order >> (4 * j)) & 15 : -1;
+      float wj = 0.f;
+#pragma unroll
+      for (int i = 0; i < EM; ++i)
+        if (i == e) wj = w[i];
+      p.idx[t * p.k + j] = e;
+      p.gate[t * p.k + j] = p.scale * (f * wj);
+    }
+  }
+  if (bad && p.status) atomicOr(p.status, MOE_STATUS_BAD_LOGIT);
+}
+
 struct RouteBwdParams {
   int64_t T;
   int E, k;
@@ -910,8 +1066,26 @@ void launch_route_v(const RouteParams& p, bool vec, cudaStream_t s) {
   launch_route_m<L, V, 1>(p, s);
 }
 
+template <typename L, int EM>
+void launch_route_few(const RouteParams& p, cudaStream_t s) {
+  const int64_t want = (p.T + kFewThreads - 1) / kFewThreads, most = static_cast<int64_t>(num_sms()) * 16;
+  const dim3 grid(static_cast<unsigned>(want < most ? want : most)), block(kFewThreads);
+  if (p.by_logit) launch_pdl(route_few_kernel<L, EM, true>, grid, block, 0, s, p);
+  else launch_pdl(route_few_kernel<L, EM, false>, grid, block, 0, s, p);
+}
+
 template <typename L>
 void launch_route_t(const RouteParams& p, cudaStream_t s) {
+  // A thread per token, for a warp per token (us, fp32 logits, tokens x experts and choices):
+  //   by the logits, softmax:        4096 x 8, 2: 2.4, 3.5; 65536 x 8, 2: 4.6, 17.0;
+  //                                  1024 x 16, 4: 3.8, 2.9; 4096 x 16, 4: 3.9, 3.7
+  //   by scores and a bias, sigmoid: 4096 x 8, 2: 5.9, 4.6; 65536 x 8, 2: 9.7, 18.7;
+  //     4 groups:                    16384 x 16, 4: 15.0, 10.5; 65536 x 16, 4: 16.7, 27.9
+  if (p.E <= 16 && p.T >= (p.by_logit ? 4096 : 32768)) {
+    if (p.E <= 8) launch_route_few<L, 8>(p, s);
+    else launch_route_few<L, 16>(p, s);
+    return;
+  }
   const bool vec = p.gs % 4 == 0;
   const int per = vec ? (p.gs + 4 * p.lanes - 1) / (4 * p.lanes) * 4
                       : (p.gs + p.lanes - 1) / p.lanes;

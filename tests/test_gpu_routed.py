@@ -247,6 +247,56 @@ def test_route_nan_and_inf_are_masked_and_reported(moe, dtype):
         assert not bool((idx == 9).any())
 
 
+FEW = [
+    # E, k, groups, top_groups, group_top
+    (1, 1, 1, 1, 1), (5, 3, 1, 1, 1), (8, 2, 1, 1, 1), (8, 4, 4, 2, 1), (12, 3, 3, 2, 2),
+    (15, 4, 5, 2, 1), (16, 16, 1, 1, 1), (16, 4, 8, 3, 2), (16, 6, 2, 1, 2), (13, 2, 13, 4, 1),
+]
+
+
+@pytest.mark.parametrize("dtype", DTYPES, ids=["f32", "bf16"])
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("shape", FEW, ids=[str(s) for s in FEW])
+def test_route_few_experts(moe, shape, score, dtype):
+    """Long batches over few experts: empty and short rows, ties, a masked expert, NaN and +inf.
+    403 rows are repeated to a batch, and every repetition gives the same bits."""
+    E, k, G, tg, gt = shape
+    n, T = 403, 33001
+    g = torch.Generator().manual_seed(E * 100 + k)
+    x = 1.5 * torch.randn(n, E, generator=g)
+    x[1::3] = torch.round(2 * x[1::3]) / 2 + 0.125               # equal logits, none opposite
+    x[2::5] = x[2::5].masked_fill(torch.rand(len(x[2::5]), E, generator=g) < 0.6, -math.inf)
+    x[3::97] = torch.finfo(torch.bfloat16).min
+    x[4::101] = -200.0                                           # scores that underflow in fp32
+    x = x.to(dtype)
+    b = 0.1 * torch.randn(E, generator=g)
+    kw = dict(score=score, groups=G, top_groups=tg, group_top=gt)
+    bm = b.clone()
+    bm[E // 2] = -math.inf
+    rows = torch.arange(T) % n
+
+    def check(bias, renorm, status=0):
+        cfg = moe.make_route_config(T, E, k, dtype=dtype, score=score, num_groups=G, top_groups=tg,
+                                    group_top=gt, renorm=renorm, scale=1.5)
+        st = status_word()
+        idx, gate = moe.route(cfg, x[rows].cuda(), None if bias is None else bias.cuda(), status=st)
+        ri, rw = ref.route(x, k, bias=bias, score=score, groups=G, top_groups=tg, group_top=gt,
+                           renorm=renorm, scale=1.5)
+        assert int(st) == status
+        idx, gate = idx.cpu(), gate.cpu()
+        assert torch.equal(idx, ri[rows])
+        assert torch.equal(gate, gate[:n][rows])
+        err = (gate[:n].double() - rw).abs()
+        assert bool((err <= 128 * U * rw.abs() + 1e-37).all()), float(err.max())
+
+    for renorm in (False, True):
+        for bias in (None, b, bm):
+            check(bias, renorm)
+    x[11, E - 1], x[n - 1, 0] = math.nan, math.inf
+    check(None, False, moe.STATUS_BAD_LOGIT)
+    check(b, True, moe.STATUS_BAD_LOGIT)
+
+
 def test_route_wide_ranges(moe):
     """Saturated sigmoids, peaked softmaxes and large biases: fp64 still decides rightly."""
     g = torch.Generator().manual_seed(2)
