@@ -80,7 +80,8 @@ enum moe_status_bits {
   MOE_STATUS_BAD_INDEX = 8,  /* bounds-checked build only (moe_bounds_checked() == 1):
                                 moe_dispatch / moe_combine and their backward passes met
                                 an expert index outside 0..E-1 or a slot outside 0..C-1;
-                                that choice skipped.  moe_route_backward: an index
+                                that choice skipped; moe_route formed an expert index
+                                outside 0..E-1, not read.  moe_route_backward: an index
                                 outside -1..E-1 (in every build), skipped             */
   MOE_STATUS_BAD_LOGIT = 16, /* moe_route: a logit or bias was NaN or +inf; that expert
                                 was masked                                            */
@@ -170,13 +171,14 @@ const char* moe_error_string(int32_t code);
 const char* moe_last_error(void);
 
 /* 1 if this library was built with bounds checks (MOE_CHECK_BOUNDS: the file
- * libmoe_b200_checked.so), else 0.  In that build moe_dispatch,
- * moe_combine and their backward passes check every expert index and slot they are given against E and
- * C before they touch a row, skip a choice that is out of range and report
- * it as MOE_STATUS_BAD_INDEX; the expert-parallel calls always check their
- * rows (MOE_STATUS_BAD_COUNTS).  A debugging aid for callers that build the
- * routing arrays themselves: the default build trusts them, as the layer's
- * own kernels produce them in range. */
+ * libmoe_b200_checked.so), else 0.  In that build moe_dispatch, moe_combine
+ * and their backward passes check every expert index and slot they are given
+ * against E and C before they touch a row, skip a choice that is out of range
+ * and report it as MOE_STATUS_BAD_INDEX; moe_route checks the experts that its
+ * own selection forms before it reads their logits and biases; the
+ * expert-parallel calls always check their rows (MOE_STATUS_BAD_COUNTS).  A
+ * debugging aid for callers that build the routing arrays themselves: the
+ * default build trusts them, as the layer's own kernels produce them in range. */
 int32_t moe_bounds_checked(void);
 
 /* Limit of every bounded wait inside the library's kernels, in ns, for the

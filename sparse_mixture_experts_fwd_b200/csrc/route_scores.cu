@@ -69,6 +69,27 @@ struct RouteParams {
 MOE_DEV float to_float(float v) { return v; }
 MOE_DEV float to_float(__nv_bfloat16 v) { return __bfloat162float(v); }
 
+// A row's logit and an expert's bias, where the expert comes out of a key.  The
+// bounds-checked build reports one outside 0..E-1 and does not read there.
+MOE_DEV bool expert_ok(const RouteParams& p, int e) {
+#if MOE_CHECK_BOUNDS
+  if (e < 0 || e >= p.E) {
+    if (p.status) atomicOr(p.status, MOE_STATUS_BAD_INDEX);
+    return false;
+  }
+#else
+  (void)p, (void)e;
+#endif
+  return true;
+}
+template <typename L>
+MOE_DEV float logit_at(const RouteParams& p, const L* h, int e) {
+  return expert_ok(p, e) ? to_float(h[e]) : 0.f;
+}
+MOE_DEV float bias_at(const RouteParams& p, int e) {
+  return expert_ok(p, e) ? __ldg(p.bias + e) : 0.f;
+}
+
 MOE_DEV bool counts(float x) { return x > kLowest && x < INFINITY; }  // false for NaN
 
 MOE_DEV float warp_max(float v) {
@@ -262,7 +283,7 @@ __device__ __noinline__ void finish_exact(const RouteParams& p, int64_t t,
     inv = warp_sum(inv);
     inv = inv > 0.f ? 1.0f / inv : 0.f;
   }
-  const float w = choice_weight(p, e >= 0 ? to_float(h[e]) : -INFINITY, m, inv);
+  const float w = choice_weight(p, e >= 0 ? logit_at(p, h, e) : -INFINITY, m, inv);
   if (lane < p.k) {
     p.idx[t * p.k + lane] = e;
     p.gate[t * p.k + lane] = w;
@@ -402,16 +423,19 @@ MOE_DEV void check_inputs(const RouteParams& p, const L* h, bool has_bias, unsig
   const bool there = rel >= 0 && rel < p.k && mine != 0u;
   const uint32_t after = __shfl_down_sync(kFull, mine, 1);
   const int e = there ? expert_of(mine) : 0;
-  const float x = there ? to_float(h[e]) : 0.f, b = there && has_bias ? __ldg(p.bias + e) : 0.f;
+  const float x = there ? logit_at(p, h, e) : 0.f, b = there && has_bias ? bias_at(p, e) : 0.f;
   const float xa = __shfl_down_sync(kFull, x, 1), ba = __shfl_down_sync(kFull, b, 1);
   close = close && after != 0u && !(x == xa && b == ba);
+  // With nothing left here there is nothing to compare; `last` is then no expert's key
+  // either where the whole row ran out before k choices.
+  if (list.head == 0u) edge = false;
   if (edge) {
     const int el = expert_of(last);
-    const float xl = to_float(h[el]), bl = has_bias ? __ldg(p.bias + el) : 0.f;
+    const float xl = logit_at(p, h, el), bl = has_bias ? bias_at(p, el) : 0.f;
     edge = false;
     while (list.head != 0u && (last >> 9) - (list.head >> 9) <= near) {
       const int en = expert_of(list.head);
-      edge |= to_float(h[en]) != xl || (has_bias && __ldg(p.bias + en) != bl);
+      edge |= logit_at(p, h, en) != xl || (has_bias && bias_at(p, en) != bl);
       list.take(list.head);
     }
   }
@@ -437,8 +461,8 @@ MOE_DEV bool settle_order(const RouteParams& p, const L* h, bool has_bias, unsig
   const int e = expert_of(cand);
   double c = -INFINITY;
   if (cand != 0u) {
-    const double x = to_float(h[e]);
-    c = MODE == kByLogit ? x : 1.0 / (1.0 + exp(-x)) + (has_bias ? __ldg(p.bias + e) : 0.f);
+    const double x = logit_at(p, h, e);
+    c = MODE == kByLogit ? x : 1.0 / (1.0 + exp(-x)) + (has_bias ? bias_at(p, e) : 0.f);
   }
   int rank = 0;
   for (int i = 0; i < n; ++i) {
@@ -472,8 +496,8 @@ MOE_DEV bool settle_groups(const RouteParams& p, const L* h, bool has_bias, unsi
     const int e = expert_of(a);
     double c = -INFINITY;
     if (a != 0u) {
-      const double x = to_float(h[e]);
-      c = MODE == kByLogit ? x : 1.0 / (1.0 + exp(-x)) + (has_bias ? __ldg(p.bias + e) : 0.f);
+      const double x = logit_at(p, h, e);
+      c = MODE == kByLogit ? x : 1.0 / (1.0 + exp(-x)) + (has_bias ? bias_at(p, e) : 0.f);
     }
     v[i] = c;
   }
@@ -659,8 +683,8 @@ route_kernel(const __grid_constant__ RouteParams p) {
       if constexpr (!kExactKey) {
         // neighbours in the order, and the last choice against what this lane has left
         const uint32_t after = __shfl_down_sync(kFull, mine, 1);
-        // (whole keys: the experts' bits only widen it, and a 0 in place of a key is
-        // sorted out below)
+        // (whole keys: the experts' bits only widen it, and check_inputs sorts out a 0 in
+        // place of a key)
         bool close = static_cast<unsigned>(rel) < static_cast<unsigned>(p.k - 1) &&
                      mine - after < (kNear + 1) << 9;
         bool edge = last - list.head < (kNear + 1) << 9;
@@ -685,7 +709,7 @@ route_kernel(const __grid_constant__ RouteParams p) {
     const bool in = my_slot < in_batch && my_j < p.k;
     const L* h = rows + static_cast<int64_t>(done) * p.E;
     const int e = in && mine ? expert_of(mine) : -1;
-    const float xj = e >= 0 ? to_float(h[my_slot * p.E + e]) : -INFINITY;
+    const float xj = e >= 0 ? logit_at(p, h + my_slot * p.E, e) : -INFINITY;
     const float w = choice_weight(p, xj, my_m, my_inv);
     if (in && !((open >> my_slot) & 1u)) {
       const int64_t o = (tb + done) * p.k + my_slot * p.k + my_j;

@@ -832,3 +832,57 @@ def test_route_offsets_past_32_bits(moe):
     assert int(idx[:-64].abs().max()) == 0
     d = moe.route_backward(cfg, x, idx, gate)
     assert torch.equal(d[-64:], moe.route_backward(one, tail, ti, tg))
+
+
+CHECKED_ROUTE = """
+import math, sys
+sys.path.insert(0, ROOT)
+sys.path.insert(0, ROOT + "/tests")
+import torch
+import sparse_mixture_experts_fwd_b200 as moe
+if moe.lib.moe_bounds_checked() != 1:
+    sys.exit(3)
+import routed_ref as ref
+g = torch.Generator().manual_seed(31)
+T = 24
+for E, k, G, tg, gt in ((48, 6, 1, 1, 1), (48, 6, 4, 2, 2), (48, 6, 4, 2, 1), (7, 7, 1, 1, 1),
+                        (255, 16, 5, 2, 2), (33, 4, 1, 1, 1), (2, 1, 1, 1, 1)):
+    x = torch.randn(T, E, generator=g)
+    x[torch.rand(T, E, generator=g) < 0.5] = -math.inf
+    x[4::5] = -math.inf                      # nothing left
+    x[5::7, 1:] = torch.finfo(torch.bfloat16).min
+    x[T - 2:] = -math.inf                    # the last rows of the buffer too
+    near = x.clone()                         # candidates that only fp64 can order
+    near[:T // 2] = torch.where(x[:T // 2] > -1, 0.5 + 2.0 ** -20 * torch.arange(E), x[:T // 2])
+    b = 0.1 * torch.randn(E, generator=g)
+    bm = b.clone()
+    bm[E // 3:] = -math.inf                  # masked for every token
+    for dt in (torch.float32, torch.bfloat16):
+        for logits in (x.to(dt), near.to(dt)):
+            for bias in (None, b, bm):
+                for score in ("softmax", "sigmoid"):
+                    kw = dict(score=score, top_groups=tg, group_top=gt)
+                    cfg = moe.make_route_config(T, E, k, num_groups=G, dtype=dt, **kw)
+                    st = torch.zeros(1, dtype=torch.int32, device="cuda")
+                    idx, gate = moe.route(cfg, logits.cuda(), None if bias is None else bias.cuda(),
+                                          status=st)
+                    ri, rw = ref.route(logits, k, bias=bias, groups=G, **kw)
+                    assert int(st) == 0, (E, score, dt, int(st))
+                    assert torch.equal(idx.cpu(), ri)
+                    assert bool((ri == -1).any()) or k == 1
+                    assert bool(((gate.cpu().double() - rw).abs() <= 2.0 ** -17 * rw + 1e-37).all())
+print("CHECKED_OK")
+"""
+
+
+def test_route_stays_inside_its_rows(cuda_device):
+    """Rows with fewer experts left than choices, in the bounds-checked build: no expert index
+    outside the row is formed for a read of the logits or of the bias (the status stays 0)."""
+    import os
+    import subprocess
+    import sys
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", f"ROOT = {root!r}\n" + CHECKED_ROUTE],
+                       capture_output=True, text=True, timeout=300,
+                       env={**os.environ, "MOE_B200_CHECK_BOUNDS": "1"})
+    assert r.returncode == 0 and "CHECKED_OK" in r.stdout, r.stdout + r.stderr
