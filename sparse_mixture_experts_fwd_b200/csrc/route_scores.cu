@@ -37,14 +37,19 @@ constexpr float kLowest = -3.3895313892515355e38f;
 enum RouteMode { kByLogit = 0, kBySigmoid = 1, kBySoftmax = 2 };
 
 // Candidates whose keys (23-bit values, see route_kernel) are this close are
-// not told apart by fp32.  In units of the key, for a pair:
+// not told apart by fp32.  In units of the key (at most 2^-23 of a score), for a pair:
 //   logits: m - x and the key each rounded once, 0.75 a candidate: under 2;
 //   sigmoid: the bias part of the key 1.5, the key's rounding 0.5, the score
 //     s (1 - s) (2^-22 + 1.5 |x| 2^-24) + s 2^-23 <= 1.7 a candidate: under 8;
-//   softmax: 2 + 2.5 (the exponential) a candidate, and the common factor 1 / sum
-//     (13 additions, their terms, a reciprocal: 20 * 2^-24) times at most 1: under 20.
-__host__ __device__ constexpr unsigned near_units(int mode) {
-  return mode == kByLogit ? 4u : mode == kBySigmoid ? 12u : 24u;
+//   softmax: bias and key 2 a candidate, as above.  With u = 2^-24, z = m - x and p the
+//     scores (the pair's sum to at most 1): the exponentials (4 u + 2.2 u z) p, 2.8 for both;
+//     their products with 1 / sum, u p, 0.5; and 1 / sum itself, which moves the pair by at
+//     most its relative error: V + 4 additions (V - 1 in a lane, 5 over the warp), the
+//     terms' 4 u + 2.2 u z averaged by p (z averaged, times the larger p, is at most 1.5
+//     for 256 experts), a reciprocal, (V + 12.3) u.  In all 17.5 for 8 logits a lane, 21.5
+//     for 16.
+__host__ __device__ constexpr unsigned near_units(int mode, int V) {
+  return mode == kByLogit ? 4u : mode == kBySigmoid ? 12u : V <= 8 ? 24u : 28u;
 }
 
 struct RouteParams {
@@ -548,7 +553,7 @@ route_kernel(const __grid_constant__ RouteParams p) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int q = lane / p.lanes, li = lane & (p.lanes - 1);
   constexpr bool kExactKey = MODE == kByLogit && sizeof(L) == 2;  // a bf16 logit fits the key
-  constexpr unsigned kNear = near_units(MODE);
+  constexpr unsigned kNear = near_units(MODE, V);
   const bool has_bias = MODE != kByLogit && p.bias != nullptr;
   const bool sums = !p.sigmoid && (MODE == kBySoftmax || !p.renorm);  // weights need 1 / sum
   bool bad = false;

@@ -151,6 +151,37 @@ def test_route_twins(moe, score, dtype):
                 check_route(moe, y, min(k, 12), b, score=score, groups=8, top_groups=3, group_top=gt)
 
 
+@pytest.mark.parametrize("shape", [(255, 5, 2, 2), (240, 3, 2, 2), (252, 9, 9, 1), (256, 1, 1, 1)],
+                         ids=str)
+@pytest.mark.parametrize("top", [0.05, 0.6], ids=["flat", "peaked"])
+def test_route_softmax_and_bias_make_near_sums(moe, shape, top):
+    """Softmax scores whose sums with the bias come in pairs, a large part of them closer than fp32
+    shows (2^-23 and below), for layers of 8 and of up to 16 logits a lane: flat rows, and rows of
+    one likely expert and many unlikely ones, whose sum is most wrong.  The likely expert's
+    neighbour in the order has little score and a large bias, so that the sum's error moves one of
+    them and not the other."""
+    E, G, tg, gt = shape
+    g = torch.Generator().manual_seed(E + int(100 * top))
+    T, k = 60, 8
+    s = torch.rand(T, E, generator=g, dtype=torch.float64) + 0.5
+    s[:, E - 1] = 0
+    s = 0.9 * (1 - top) * s / s.sum(1, keepdim=True)
+    b = torch.empty(E)
+    n = E // 2
+    b[0::2] = 0.02 * torch.rand(E - n, generator=g)
+    even = b[0::2][:n].double() + s[:, 0:2 * n:2]
+    b[1::2] = (even.mean(0) - s[:, 1::2].mean(0)).float()
+    s[:, 1::2] = (even - b[1::2].double()).clamp(min=1e-4)        # s + b of a pair: equal
+    b[0], b[E - 1] = top, 0.0
+    s[:, E - 1] = s[:, 0] + b[0].double()
+    b[1], s[:, 1] = -1.0, 0
+    s[:, 1] = 1 - s.sum(1)                                        # never chosen; the sum is 1
+    assert float(s.min()) > 0
+    x = s.log().float()                                           # ... up to the logits' rounding
+    check_route(moe, x, k, b, score="softmax", groups=G, top_groups=tg, group_top=gt)
+    check_route(moe, x, 1, b, score="softmax", groups=G, top_groups=tg, group_top=gt)
+
+
 def test_route_border_hidden_behind_equal_ones(moe):
     """Many exactly equal candidates at the last place, and one that differs from them by less
     than fp32 shows (its bias makes up for a smaller logit)."""
