@@ -254,9 +254,11 @@ int32_t moe_topk_assign(const moe_config* cfg, const float* logits, const int32_
  *     largest c (of those that can be chosen); the top_groups best groups stay
  *   expert_idx[t, :] = the k largest c of the groups that stay, descending
  *   gate[t, j] = scale * s[t, e_j], renorm: divided by sum_i s[t, e_i]
- * Ties go to the lower group and the lower expert.  The order is that of the
- * exact values: fp32 decides where it can, fp64 where two candidates are too
- * close for it; without a bias the logits themselves are compared.
+ * Ties go to the lower group and the lower expert.  Without a bias, and unless
+ * groups are limited by sums of two, the logits themselves are compared.  Else
+ * the order is that of c, and of its sums, in fp64 (fp32 decides where it
+ * can): values that fp64 rounds to one number are ties, such as the sigmoids
+ * of logits above 38 or softmax scores 746 below the row's largest logit.
  * Masks: a logit of -inf, or at or below bf16's lowest value (-3.3895e38; so
  * fp32's lowest too), masks the expert for that token (score 0), a bias of
  * -inf masks it for every token; NaN and +inf are treated the same and set

@@ -341,7 +341,8 @@ def make_route_config(T, E, k, *, score="softmax", num_groups=1, top_groups=None
 def route(rcfg, logits, bias=None, expert_idx=None, gate=None, status=None, stream=None):
     """Choices and weights from router logits [T, E]: (expert_idx [T, k] int32, gate [T, k] fp32).
 
-    ``bias`` [E] fp32 enters the choice only.  A token with fewer than k experts
+    ``bias`` [E] fp32 enters the choice only.  Ties go to the lower group and expert; with a
+    bias or group values of two experts, scores that fp64 cannot tell apart are ties.  A token with fewer than k experts
     left (the others masked by -inf) gets -1 and weight 0 for the rest."""
     T, E, k = rcfg.T, rcfg.E, rcfg.k
     lp = _arg(logits, "logits", _act_dtype(rcfg), (T, E))

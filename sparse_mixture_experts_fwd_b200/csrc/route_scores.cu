@@ -7,9 +7,9 @@
 //   choices = the k largest c of the groups that stay (ties -> lower expert)
 //   w[t, j] = scale * s[t, e_j] / (renorm ? sum_i s[t, e_i] : 1)
 //
-// The order is that of the real numbers, not of their fp32 roundings: without
-// a bias it is the logits' own order, and where fp32 cannot tell two
-// candidates apart they are ranked in fp64.
+// The order is not that of fp32 roundings: without a bias and sums of two it is the
+// logits' own order, else that of c and its sums in fp64, which ranks the candidates
+// that fp32 cannot tell apart (scores that saturate in fp64 too are ties).
 //
 // Bound by instruction issue: 65536 x 256 fp32 logits, 8 experts in 4 of 8 groups by
 // sigmoid scores with a bias, 39.9 us, about 470 warp instructions a token; the

@@ -342,6 +342,28 @@ def test_route_wide_ranges(moe):
         check_route(moe, x.clamp(-15, 15), 8, 1e4 * b, score=score)
 
 
+def test_route_scores_that_saturate_are_ties(moe):
+    """Where scores decide (a bias, or group values of two experts) what fp64 rounds to the same
+    number is a tie; where they do not, the logits' order holds however far the scores saturate."""
+    x = torch.full((3, 16), -5.0)
+    x[0, 4:8] = torch.tensor([40.0, 39.0, 60.0, 50.0])     # sigmoids: all 1.0 in fp64
+    x[1, 4:8] = torch.tensor([30.0, 29.0, 31.0, 30.5])     # told apart by fp64 only
+    x[2, 8:12] = torch.tensor([-790.0, -780.0, -760.0, -770.0])   # sigmoids and softmax scores: 0
+    x[2, :8] = -900.0
+    x[2, 12:] = -800.0
+    kw = dict(score="sigmoid", groups=4, top_groups=1)
+    two, _ = check_route(moe, x, 4, group_top=2, **kw)
+    one, _ = check_route(moe, x, 4, group_top=1, **kw)
+    biased, _ = check_route(moe, x, 4, torch.full((16,), 0.125), group_top=1, **kw)
+    assert two[0].tolist() == biased[0].tolist() == [4, 5, 6, 7] and one[0].tolist() == [6, 7, 4, 5]
+    assert two[1].tolist() == biased[1].tolist() == one[1].tolist() == [6, 7, 4, 5]
+    assert two[2].tolist() == biased[2].tolist() == [0, 1, 2, 3] and one[2].tolist() == [10, 11, 9, 8]
+    x[2, 0] = 0.0                                          # the others' softmax scores underflow
+    two, _ = check_route(moe, x[2:], 3, score="softmax", groups=4, top_groups=2, group_top=2)
+    one, _ = check_route(moe, x[2:], 3, score="softmax", groups=4, top_groups=2, group_top=1)
+    assert two[0].tolist() == [0, 1, 2] and one[0].tolist() == [0, 10, 11]
+
+
 def test_route_empty_batch_and_refusals(moe):
     cfg = moe.make_route_config(0, 16, 4)
     idx, gate = moe.route(cfg, torch.empty(0, 16, device="cuda"))
