@@ -163,7 +163,11 @@ def _ptr(t, name):
     return t.data_ptr()
 
 
-_current_device, _current_stream = torch._C._cuda_getDevice, torch._C._cuda_getCurrentRawStream
+# torch's own handles where they are there (a torch built without CUDA has none: then the first
+# call raises torch's error, as its public functions do)
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+_current_stream = getattr(torch._C, "_cuda_getCurrentRawStream",
+                          lambda device: torch.cuda.current_stream(device).cuda_stream)
 
 
 def _stream(stream=None) -> int:

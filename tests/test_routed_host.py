@@ -164,3 +164,34 @@ def test_binding_refuses_cpu_tensors(moe):
         moe.assign(cfg, torch.zeros(4, 7, dtype=torch.int32))
     with pytest.raises(TypeError, match="expert_idx"):
         moe.assign(cfg, torch.zeros(4, 8, dtype=torch.int64))
+
+
+WITHOUT_CUDA = """
+import sys
+sys.path.insert(0, ROOT)
+import torch
+for name in ("_cuda_getDevice", "_cuda_getCurrentRawStream"):
+    if hasattr(torch._C, name):
+        delattr(torch._C, name)
+import sparse_mixture_experts_fwd_b200 as moe
+class Stream:
+    cuda_stream = 4096
+asked = []
+torch.cuda.current_stream = lambda device=None: (asked.append(device), Stream)[1]
+torch.cuda.current_device = moe._current_device = lambda: 3
+assert moe._stream() == 4096 and asked == [3]
+assert moe.capacity(256, 8, 1.0) == 32
+print("IMPORT_OK")
+"""
+
+
+def test_import_without_torchs_cuda_handles():
+    """A torch without them (one built without CUDA) still imports the package, and the current
+    stream then comes from torch's public functions."""
+    import os
+    import subprocess
+    import sys
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", f"ROOT = {root!r}\n" + WITHOUT_CUDA],
+                       capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0 and "IMPORT_OK" in r.stdout, r.stdout + r.stderr
