@@ -264,7 +264,11 @@ int32_t moe_topk_assign(const moe_config* cfg, const float* logits, const int32_
  * -inf masks it for every token; NaN and +inf are treated the same and set
  * MOE_STATUS_BAD_LOGIT.  A masked expert is never chosen: a token with fewer
  * than k experts left gets expert_idx -1 and gate 0 for the rest (moe_assign
- * drops such a choice).  Outputs [T, k]: expert_idx int32, gate fp32. */
+ * drops such a choice).  Outputs [T, k]: expert_idx int32, gate fp32, within
+ * 128 units of 2^-24 of the formula.  The same call gives the same bits; for at
+ * most 16 experts a row's gates may differ in the last bits between short and
+ * long batches (from 4096 tokens, or 32768 where scores decide), which other
+ * kernels form. */
 int32_t moe_route(const moe_route_config* cfg, const void* logits, const float* bias,
                   int32_t* expert_idx, float* gate, int32_t* status, moe_stream_t stream);
 

@@ -694,7 +694,10 @@ def adamw_state(params, bits=32):
 
 class AdamWTensors:
     """The tensors of an AdamW step, checked and laid out once (``adamw_tensors``).  It holds
-    on to the tensors; a step reads and writes the memory they had when it was made."""
+    on to the tensors; a step reads and writes the memory they had when it was made, the
+    gradients' too.  Where a backward pass puts its gradients into new tensors, copy them into
+    these or make a new layout: a step on this one would take the old gradients, without an
+    error, since they are kept alive here."""
 
     def __init__(self, n, device, grad_dtype, bits, arrays, keep):
         self.n, self.device, self.grad_dtype, self.bits = n, device, grad_dtype, bits
@@ -707,7 +710,10 @@ def adamw_tensors(params, grads, exp_avg, exp_avg_sq, *, exp_avg_scale=None,
     the moments fp32, or float8_e4m3fn with their fp32 scales (one per 256 elements);
     ``bf16_copies`` (optional, entries may be None) receive the new parameters in bf16.  All
     contiguous, on one device, with the parameter's number of elements; nothing that the
-    step writes may overlap anything else."""
+    step writes may overlap anything else.
+
+    For buffers that stay where they are over the training (gradients zeroed or overwritten in
+    place, not set to None): the checks cost some 7 us a tensor, a step on the result none of it."""
     params, grads = list(params), list(grads)
     n = len(params)
     dev = params[0].device if n else None
