@@ -713,7 +713,7 @@ def adamw_tensors(params, grads, exp_avg, exp_avg_sq, *, exp_avg_scale=None,
     step writes may overlap anything else.
 
     For buffers that stay where they are over the training (gradients zeroed or overwritten in
-    place, not set to None): the checks cost some 7 us a tensor, a step on the result none of it."""
+    place, not set to None): the checks cost 3 to 7 us a tensor once, and the steps nothing."""
     params, grads = list(params), list(grads)
     n = len(params)
     dev = params[0].device if n else None

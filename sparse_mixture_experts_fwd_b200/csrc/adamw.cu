@@ -419,9 +419,9 @@ struct Stage8 {
 
 // A warp takes a chunk of up to 8 consecutive blocks: their scales are one
 // 32-byte sector, loaded and stored at once by 8 lanes.  (One 4-byte store per
-// block costs 100 of 520 us on 184 M parameters: partial sectors.)  With bf16
-// gradients, 2.6 GB: 440 us at full clocks, 0.9 of the copy rate; issue-bound (0.71 of
-// the slots), and 485 once the board's power cap lowers the clock.
+// block cost 80 of 522 us on 184 M parameters: partial sectors.)  With bf16
+// gradients, 2.6 GB: 440 us at full clocks, 0.9 of the copy rate; issue-bound (0.75 of
+// the slots), and 490 once the board's power cap lowers the clock.
 template <typename G, int N>
 __global__ void __launch_bounds__(kThreads, 3)
 adamw8_kernel(const __grid_constant__ AdamBatch<N> b, const AdamHyper h) {

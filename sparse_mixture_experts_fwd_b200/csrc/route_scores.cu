@@ -12,7 +12,7 @@
 // that fp32 cannot tell apart (scores that saturate in fp64 too are ties).
 //
 // Bound by instruction issue: 65536 x 256 fp32 logits, 8 experts in 4 of 8 groups by
-// sigmoid scores with a bias, 39.9 us, about 470 warp instructions a token; the
+// sigmoid scores with a bias, 40 us, 493 warp instructions a token; the
 // logits' bytes alone would take 10.9.  4 tokens: 4.0 us.  Layers of few experts take
 // a thread per token (route_few_kernel).
 #include <cfloat>
@@ -529,7 +529,11 @@ MOE_DEV bool settle_groups(const RouteParams& p, const L* h, bool has_bias, unsi
 // (settle_order, settle_groups).  What that leaves open (softmax scores with a
 // bias, whose sum is needed in fp64 too; a third candidate close to a group's
 // two) is listed, and the block's warps decide it at the end (finish_exact),
-// side by side.
+// side by side.  What that costs, 65536 x 256, us: by sigmoid scores and groups 40 for
+// random logits, 67 where every expert has a twin one step away (candidates settled
+// alone), 300 where every token goes to finish_exact (such as a group of which one
+// expert is left, with sums of two); softmax scores with a bias 47 and, with twins,
+// 290; by the logits 31 and 50.
 //
 // The scores here only decide, so they take the hardware's exp2 and reciprocal;
 // the weights of the k choices are formed from their logits with expf.  That
