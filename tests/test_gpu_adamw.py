@@ -364,3 +364,27 @@ def test_router_weights_are_trained(moe):
     p, m, v = ref.adamw(before, dW.cpu(), zero, zero, step=1, coef=0.5, **HYPER)
     assert bool(((W.cpu().double() - p).abs() <= 4 * U * p.abs() + 24 * U * HYPER["lr"]).all())
     assert torch.equal(Wr, W.bfloat16())
+
+
+@pytest.mark.parametrize("bits", [32, 8])
+def test_elements_past_32_bits(moe, bits):
+    """A tensor of more than 2^31 elements (30 and 17 GB in all): its last elements come out as
+    those of a short tensor do, which sees nothing of the others."""
+    n, tail, dev = 2 ** 31 + 1000, 2024, "cuda"     # the tail starts at a block of 256
+    gen = torch.Generator(device=dev).manual_seed(4)
+    p = torch.zeros(n, device=dev)
+    g = torch.zeros(n, dtype=torch.bfloat16, device=dev)
+    p[-tail:].normal_(generator=gen)
+    g[-tail:].normal_(generator=gen)
+    state = moe.adamw_state([p], bits)
+    q, h = p[-tail:].clone(), g[-tail:].clone()
+    short = moe.adamw_state([q], bits)
+    whole, part = moe.adamw_tensors([p], [g], **state), moe.adamw_tensors([q], [h], **short)
+    for step in (1, 2):
+        moe.adamw_step(whole, step=step, **HYPER)
+        moe.adamw_step(part, step=step, **HYPER)
+    assert (n - tail) % 256 == 0
+    assert torch.equal(p[-tail:], q) and not bool(torch.equal(q, torch.zeros_like(q)))
+    for name, v in short.items():
+        assert torch.equal(state[name][0][-v[0].numel():].view(torch.uint8), v[0].view(torch.uint8)), name
+    assert int(torch.count_nonzero(p[:-tail])) == 0

@@ -887,6 +887,36 @@ def test_route_offsets_past_32_bits(moe):
     assert torch.equal(d[-64:], moe.route_backward(one, tail, ti, tg))
 
 
+def test_row_exchange_offsets_past_32_bits(moe):
+    """Expert rows behind element 2^31 (4.4 GB of rows): the last experts' rows come and go as in
+    a layer of those experts alone."""
+    E, C, d, T, k, last = 256, 8400, 1024, 40, 3, 4
+    g = torch.Generator().manual_seed(13)
+    assert (E - last) * C * d > 2 ** 31
+    few = torch.stack([torch.randperm(last, generator=g)[:k] for _ in range(T)]).int()
+    a = ref.assign(few, last, C)
+    slot = torch.where(a["kept"] != 0, a["slot"] + (C - T * k), a["slot"]).cuda()   # at the end
+    kept, few = a["kept"].cuda(), few.cuda()
+    idx = few + (E - last)
+    x = torch.randn(T, d, generator=g).bfloat16().cuda()
+    gate = torch.rand(T, k, generator=g).cuda()
+    big = moe.make_config(T, d, 64, E, k, C)
+    one = moe.make_config(T, d, 64, last, k, C)
+    xe = torch.zeros(E, C, d, dtype=torch.bfloat16, device="cuda")
+    xs = torch.zeros(last, C, d, dtype=torch.bfloat16, device="cuda")
+    moe.dispatch(big, x, idx, slot, kept, xe=xe)
+    moe.dispatch(one, x, few, slot, kept, xe=xs)
+    assert torch.equal(xe[-last:], xs) and int(torch.count_nonzero(xe[:-last])) == 0
+    assert torch.equal(moe.combine(big, xe, idx, gate, slot, kept),
+                       moe.combine(one, xs, few, gate, slot, kept))
+    assert torch.equal(moe.dispatch_backward(big, xe, idx, slot, kept),
+                       moe.dispatch_backward(one, xs, few, slot, kept))
+    _, dg = moe.combine_backward(big, x, xe, idx, gate, slot, kept, dye=xe)
+    _, ds = moe.combine_backward(one, x, xs, few, gate, slot, kept, dye=xs)
+    assert torch.equal(dg, ds) and torch.equal(xe[-last:], xs)
+    assert int(torch.count_nonzero(xe[:-last])) == 0
+
+
 CHECKED_ROUTE = """
 import math, sys
 sys.path.insert(0, ROOT)
