@@ -346,8 +346,9 @@ def route(rcfg, logits, bias=None, expert_idx=None, gate=None, status=None, stre
     """Choices and weights from router logits [T, E]: (expert_idx [T, k] int32, gate [T, k] fp32).
 
     ``bias`` [E] fp32 enters the choice only.  Ties go to the lower group and expert; with a
-    bias or group values of two experts, scores that fp64 cannot tell apart are ties.  A token with fewer than k experts
-    left (the others masked by -inf) gets -1 and weight 0 for the rest."""
+    bias or group values of two experts, scores that fp64 cannot tell apart are ties.  A token
+    with fewer than k experts left (the others masked by -inf) gets -1 and weight 0 for the
+    rest."""
     T, E, k = rcfg.T, rcfg.E, rcfg.k
     lp = _arg(logits, "logits", _act_dtype(rcfg), (T, E))
     bp = None if bias is None else _arg(bias, "bias", torch.float32, (E,))
