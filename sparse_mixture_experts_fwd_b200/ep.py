@@ -30,7 +30,7 @@ from __future__ import annotations
 import torch
 import torch.distributed as dist
 
-from . import (ROUTE_TOPK, _act_dtype, assign_workspace_size, ep_combine,
+from . import (ROUTE_TOPK, _act_dtype, assign_workspace_size, config_check, ep_combine,
                ep_dispatch, ep_ffn_config, expert_ffn, ffn_workspace_size, router, topk_assign)
 
 
@@ -98,6 +98,7 @@ class ExpertParallelLayer:
     def __init__(self, cfg, group=None, device=None, sync: str = "stream"):
         if sync not in ("stream", "host"):
             raise ValueError('sync must be "stream" or "host"')
+        config_check(cfg)  # the layer's own calls take one or two choices; ep_ffn_config more
         self.host_sync = sync == "host"
         self.group = group
         self.rank = dist.get_rank(group)

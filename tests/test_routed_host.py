@@ -166,6 +166,21 @@ def test_binding_refuses_cpu_tensors(moe):
         moe.assign(cfg, torch.zeros(4, 8, dtype=torch.int64))
 
 
+def test_expert_parallel_layer_refuses_more_choices_before_it_allocates(moe, monkeypatch):
+    """The layer takes one or two choices: three are refused with that reason, not after (or by)
+    the allocation of its buffers."""
+    from sparse_mixture_experts_fwd_b200 import ep
+    monkeypatch.setattr(ep.dist, "get_rank", lambda group=None: 0)
+    monkeypatch.setattr(ep.dist, "get_world_size", lambda group=None: 2)
+
+    def no_memory(*a, **k):
+        raise AssertionError("allocated")
+
+    monkeypatch.setattr(ep.torch, "empty", no_memory)
+    with pytest.raises(moe.MoEError, match="k must be 1 or 2"):
+        ep.ExpertParallelLayer(moe.make_config(64, 64, 64, 8, 3, 16), device="cpu")
+
+
 WITHOUT_CUDA = """
 import sys
 sys.path.insert(0, ROOT)
